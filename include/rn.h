@@ -330,6 +330,45 @@ rn_status gated_norm_bwd_static_ws(int64_t rows, int32_t width, float eps, rn_dt
                                    float* dw, rn_stream stream);
 
 /*
+ * Layer norm
+ * ----------
+ * Beside the RMS norms, under the same contract (fp32 sums in an order that
+ * depends on the width and dtype only, one rounding at the store):
+ *   mean = sum_j x_j / H,  c_j = x_j - mean,  rstd = rsqrt(sum_j c_j^2 / H + eps)
+ *   y_j = c_j * rstd * w_j + b_j
+ * The variance is the mean of the squared differences from the mean.
+ * x: [rows, width] dt, read.  w: [width] fp32, read.  b: [width] fp32, read,
+ * or NULL (no bias).  y: [rows, width] dt, written; y may be exactly x.
+ * mean, rstd: [rows] fp32, written, each or NULL.  A row's outputs are bitwise
+ * the same alone or at any position of any batch.  rows == 0 enqueues nothing.
+ */
+rn_status layernorm_fwd(int64_t rows, int32_t width, float eps, rn_dtype dt, const void* x,
+                        const float* w, const float* b, void* y, float* mean, float* rstd,
+                        rn_stream stream);
+
+/*
+ * Layer norm backward, the gradient of sum(y * dy): with xh = (x - mean) * rstd
+ * and g = w * dy,
+ *   dx = rstd * (g - mean_j(g) - xh * mean_j(g * xh)),
+ *   dw[j] = sum over rows of dy * xh,  db[j] = sum over rows of dy.
+ * mean, rstd: [rows] fp32 from layernorm_fwd, read.  row_mask: [rows] bytes,
+ * read, or NULL; rows with row_mask[r] == 0 add nothing to dw and db, whatever
+ * their values (dx is written for every row).  dx: [rows, width] dt, written;
+ * dx may be exactly dy.  dw: [width] fp32, written.  db: [width] fp32, written,
+ * or NULL to leave it out.  dw and db over no contributing row are -0.0.
+ * Their sums use no atomics: contiguous blocks of rows are summed in a fixed
+ * order and joined by the level-by-level pairwise tree; the order depends on
+ * the row count, the width and the dtype only.
+ * ws: device workspace of ws_bytes >= layernorm_bwd_workspace_bytes(rows, width,
+ * dt), 16-byte aligned, contents irrelevant (may be NULL where that is 0).
+ */
+size_t layernorm_bwd_workspace_bytes(int64_t rows, int32_t width, rn_dtype dt);
+rn_status layernorm_bwd(int64_t rows, int32_t width, rn_dtype dt, const void* x, const float* w,
+                        const void* dy, const float* mean, const float* rstd,
+                        const uint8_t* row_mask, void* dx, float* dw, float* db, void* ws,
+                        size_t ws_bytes, rn_stream stream);
+
+/*
  * Provenance record (RFC #415 section 4, point 8): a static, NUL-terminated
  * string naming the kernels, the reduction schedule and tree, and the
  * accumulator for (width, dt); "unsupported" for an invalid pair.  The

@@ -10,6 +10,8 @@ from .ops import (  # noqa: F401
     act_code,
     gated_norm_bwd,
     gated_norm_fwd,
+    layernorm_bwd,
+    layernorm_fwd,
     norm_bwd,
     norm_bwd_workspace_bytes,
     norm_fwd,

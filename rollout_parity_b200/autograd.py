@@ -62,6 +62,24 @@ class RMSNorm(torch.autograd.Function):
         return dx, dw, dz, None, None, None
 
 
+class LayerNorm(torch.autograd.Function):
+    """y = (x - mean) * rstd * w + b; x [rows, width] bf16/fp16/fp32, w and b (or
+    None) fp32 [width]."""
+
+    @staticmethod
+    def forward(ctx, x, w, b=None, eps=1e-5):
+        y, mean, rstd = ops.layernorm_fwd(x, w, b, eps)
+        ctx.save_for_backward(x, w, mean, rstd)
+        ctx.biased = b is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, mean, rstd = ctx.saved_tensors
+        dx, dw, db = ops.layernorm_bwd(x, w, dy.contiguous(), mean, rstd, want_db=ctx.biased)
+        return dx, dw, db, None
+
+
 def zero_centred_rms_norm(x, w, eps=1e-6):
     return ZeroCentredRMSNorm.apply(x, w, eps)
 
@@ -72,3 +90,7 @@ def gated_rms_norm(x, z, w, eps=1e-6):
 
 def rms_norm(x, w, z=None, eps=1e-6, weight_offset=1.0, act=None):
     return RMSNorm.apply(x, w, z, eps, weight_offset, act)
+
+
+def layer_norm(x, w, b=None, eps=1e-5):
+    return LayerNorm.apply(x, w, b, eps)

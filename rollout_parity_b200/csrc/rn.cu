@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include "rn.h"
+#include "rn_checks.cuh"
 #include "rn_common.cuh"
 #include "rn_gate.cuh"
 
@@ -217,8 +218,6 @@ int pow2ceil(int v) {
   return p;
 }
 
-bool width_ok(int32_t width) { return width >= 8 && width <= 16384 && width % 8 == 0; }
-bool dtype_ok(rn_dtype dt) { return dt == RN_F32 || dt == RN_BF16 || dt == RN_F16; }
 bool act_ok(rn_act act) { return act == RN_ACT_NONE || act == RN_ACT_SILU || act == RN_ACT_SIGMOID; }
 
 // (T, K) as a function of the width and element size only -- this is the
@@ -295,41 +294,10 @@ size_t ws_bytes_of(int64_t rows, int32_t width) {
   return size_t(g0 + g1) * size_t(width) * sizeof(float);
 }
 
-struct Range {
-  const void* p;
-  size_t n;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = uintptr_t(a.p), b0 = uintptr_t(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-bool aligned16(const void* p) { return (uintptr_t(p) & 15u) == 0; }
-
 rn_status common_checks(int64_t rows, int32_t width, float eps, rn_dtype dt) {
   if (rows < 0 || rows > kMaxRows || !std::isfinite(eps) || eps < 0.0f) return RN_E_ARG;
   if (!dtype_ok(dt)) return RN_E_DTYPE;
   if (!width_ok(width)) return RN_E_WIDTH;
-  return RN_OK;
-}
-
-// inputs: read-only ranges; outputs: written ranges.  Outputs must not overlap
-// anything else; inputs may overlap one another.  alias_out / alias_in name
-// one output that may be exactly the given input (same start, same size): an
-// in-place update, which the kernels allow because a thread reads each element
-// before it writes the same element and no other thread touches it.
-rn_status check_ranges(const Range* in, int nin, const Range* out, int nout, int alias_out = -1,
-                       int alias_in = -1) {
-  for (int i = 0; i < nout; ++i) {
-    for (int j = 0; j < nin; ++j) {
-      if (i == alias_out && j == alias_in && out[i].p == in[j].p && out[i].n == in[j].n) continue;
-      if (overlap(out[i], in[j])) return RN_E_ARG;
-    }
-    for (int j = i + 1; j < nout; ++j)
-      if (overlap(out[i], out[j])) return RN_E_ARG;
-  }
   return RN_OK;
 }
 
@@ -603,6 +571,22 @@ rn_status launch_status() {
   }
   ++t_launches;
   return RN_OK;
+}
+
+void begin_call() { t_launches = 0; }
+bool validate_only() { return g_validate_only.load() != 0; }
+rn_status cuda_failed(int code) {
+  t_last_cuda = code;
+  return RN_E_CUDA;
+}
+Sched row_sched(int32_t width, rn_dtype dt) {
+  Sched s;
+  pick_sched(width, dt, &s);
+  return s;
+}
+rn_status fill_neg_zero(float* out, int n, cudaStream_t st) {
+  k_fill_neg_zero<<<(n + 255) / 256, 256, 0, st>>>(out, n);
+  return launch_status();
 }
 
 // Dynamic shared memory of k_bwd: reduction scratch, sub-warp gain, staged

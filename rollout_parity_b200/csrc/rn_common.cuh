@@ -139,6 +139,11 @@ inline size_t elem_bytes(rn_dtype dt) { return dt == RN_F32 ? 4 : 2; }
 int sm_count();
 int grid_cap(int64_t want);
 rn_status launch_status();   // RN_OK, or RN_E_CUDA with the error recorded
+rn_status cuda_failed(int code);   // records a cudaError_t; RN_E_CUDA
+void begin_call();                 // an entry point starts: no kernel enqueued yet
+bool validate_only();              // checks only, no CUDA call (rn_test_set_validate_only)
+Sched row_sched(int32_t width, rn_dtype dt);   // the forward's (T, K) of a valid width and dtype
+rn_status fill_neg_zero(float* out, int n, cudaStream_t st);   // the empty sum, -0.0
 // dynamic shared memory of k_fwd / k_bwd (their layouts)
 size_t fwd_smem_bytes(const Sched& s, bool gated, bool resid, rn_dtype dt);
 size_t bwd_smem_bytes(const Sched& s, int lpc, int width, bool gated, rn_dtype dt);

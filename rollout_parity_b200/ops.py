@@ -398,6 +398,83 @@ def rn_fold_rows(partials: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     return out
 
 
+def _row_mask(row_mask: Optional[torch.Tensor], rows: int, device) -> Optional[torch.Tensor]:
+    if row_mask is None:
+        return None
+    if row_mask.dtype not in (torch.bool, torch.uint8) or tuple(row_mask.shape) != (rows,) \
+            or row_mask.device != device or not row_mask.is_contiguous():
+        raise ValueError(f"row_mask must be a contiguous bool/uint8 [{rows}] tensor on {device}")
+    return row_mask.view(torch.uint8)
+
+
+def _buffer(ws: Optional[torch.Tensor], need: int, device) -> Tuple[torch.Tensor, int]:
+    """A workspace of at least ``need`` bytes (the caller's is passed through)."""
+    if ws is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device), max(need, 16)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous buffer on the tensors' device")
+    return ws, ws.numel() * ws.element_size()
+
+
+def layernorm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, *, y: Optional[torch.Tensor] = None,
+                  mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                  want_stats: bool = True, stream=None):
+    """Layer norm forward y = (x - mean) * rstd * w + b (b None: no bias).
+    Returns (y, mean, rstd); the statistics are None when want_stats is False
+    and none were passed.  y may be x itself."""
+    rows, width = _rows_width(x)
+    dt = _dt(x)
+    _vec("w", w, width, x.device)
+    if b is not None:
+        _vec("b", b, width, x.device)
+    y = torch.empty_like(x) if y is None else _mat("y", y, x)
+    if want_stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if mean is None else mean
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    if mean is not None:
+        _vec("mean", mean, rows, x.device)
+    if rstd is not None:
+        _vec("rstd", rstd, rows, x.device)
+    with torch.cuda.device(x.device):
+        check("layernorm_fwd",
+              load().layernorm_fwd(rows, width, eps, dt, _ptr(x), _ptr(w), _ptr(b), _ptr(y),
+                                   _ptr(mean), _ptr(rstd), _stream(x, stream)))
+    return y, mean, rstd
+
+
+def layernorm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor,
+                  rstd: torch.Tensor, *, row_mask: Optional[torch.Tensor] = None,
+                  want_db: bool = True, dx: Optional[torch.Tensor] = None,
+                  dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None, stream=None):
+    """Layer norm backward.  Returns (dx, dw, db); db is None when want_db is
+    False and none was passed.  row_mask ([rows] bool or uint8): rows where it
+    is zero are left out of dw and db.  dx may be dy itself."""
+    rows, width = _rows_width(x)
+    dt = _dt(x)
+    _vec("w", w, width, x.device)
+    _mat("dy", dy, x)
+    _vec("mean", mean, rows, x.device)
+    _vec("rstd", rstd, rows, x.device)
+    row_mask = _row_mask(row_mask, rows, x.device)
+    dx = torch.empty_like(x) if dx is None else _mat("dx", dx, x)
+    dw = torch.empty(width, dtype=torch.float32, device=x.device) if dw is None else \
+        _vec("dw", dw, width, x.device)
+    if db is not None:
+        _vec("db", db, width, x.device)
+    elif want_db:
+        db = torch.empty(width, dtype=torch.float32, device=x.device)
+    lib = load()
+    ws, nws = _buffer(ws, int(lib.layernorm_bwd_workspace_bytes(rows, width, dt)), x.device)
+    with torch.cuda.device(x.device):
+        check("layernorm_bwd",
+              lib.layernorm_bwd(rows, width, dt, _ptr(x), _ptr(w), _ptr(dy), _ptr(mean),
+                                _ptr(rstd), _ptr(row_mask), _ptr(dx), _ptr(dw), _ptr(db),
+                                _ptr(ws), nws, _stream(x, stream)))
+    return dx, dw, db
+
+
 def rn_describe(width: int, dtype=torch.bfloat16) -> str:
     """The provenance string for (width, dtype): kernels, team shape, reduction
     order, dw tree, accumulator; "unsupported" for an invalid pair."""
