@@ -369,6 +369,40 @@ rn_status layernorm_bwd(int64_t rows, int32_t width, rn_dtype dt, const void* x,
                         size_t ws_bytes, rn_stream stream);
 
 /*
+ * Embedding
+ * ---------
+ * The first operator of a language model, with the scaling some families
+ * apply (RL-Kernel RFC #415 lists a scaled embedding), and its gradient:
+ *   y[t] = fmt(scale * table[ids[t]])        (fp32 product, one rounding)
+ *   dtable[v] = fmt(scale * sum over t with ids[t] == v of dy[t])
+ * A token whose id is outside [0, vocab) -- padding -- has a zero row in y and
+ * adds nothing to dtable.
+ * ids: [tokens] int64, read, 8-byte aligned.  table: [vocab, width] dt, read.
+ * y: [tokens, width] dt, written.  1 <= vocab <= 2^27, 0 <= tokens <= 2^28,
+ * else RN_E_ARG.
+ */
+rn_status embed_fwd(int64_t tokens, int64_t vocab, int32_t width, float scale, rn_dtype dt,
+                    const int64_t* ids, const void* table, void* y, rn_stream stream);
+
+/*
+ * Embedding gradient.  dy: [tokens, width] dt, read.  dtable: [vocab, width] dt,
+ * written: every row, zeros where no token has the id.  With accumulate != 0
+ * the sums are added to what dtable holds (one rounding: fmt(old + scale *
+ * sum)), and rows without a token are not touched: a table tied to the output
+ * projection takes the projection's gradient first.
+ * The sums are fp32 without atomics: a row's tokens are added in token order
+ * inside leaves of 32 of them, and the leaves are joined by the level-by-level
+ * pairwise tree, so a row of dtable is bitwise the same wherever its tokens
+ * stand in the batch and whatever the other tokens are.
+ * ws: device workspace of ws_bytes >= embed_bwd_workspace_bytes(tokens, width)
+ * (never 0 for valid sizes), 16-byte aligned, contents irrelevant.
+ */
+size_t embed_bwd_workspace_bytes(int64_t tokens, int32_t width);
+rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, rn_dtype dt,
+                    const int64_t* ids, const void* dy, int32_t accumulate, void* dtable, void* ws,
+                    size_t ws_bytes, rn_stream stream);
+
+/*
  * Provenance record (RFC #415 section 4, point 8): a static, NUL-terminated
  * string naming the kernels, the reduction schedule and tree, and the
  * accumulator for (width, dt); "unsupported" for an invalid pair.  The

@@ -8,6 +8,8 @@ torch.autograd Functions; ``workloads`` draws seeded synthetic inputs.
 from ._lib import LIB_PATH, Act, DType, RNError, Status, load  # noqa: F401
 from .ops import (  # noqa: F401
     act_code,
+    embed_bwd,
+    embed_fwd,
     gated_norm_bwd,
     gated_norm_fwd,
     layernorm_bwd,

@@ -80,6 +80,22 @@ class LayerNorm(torch.autograd.Function):
         return dx, dw, db, None
 
 
+class Embedding(torch.autograd.Function):
+    """y[t] = scale * table[ids[t]]; ids [tokens] int64, table [vocab, width]
+    bf16/fp16/fp32.  The gradient of the table is dense."""
+
+    @staticmethod
+    def forward(ctx, ids, table, scale=1.0):
+        ctx.save_for_backward(ids)
+        ctx.vocab, ctx.scale = table.shape[0], scale
+        return ops.embed_fwd(ids, table, scale)
+
+    @staticmethod
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        return None, ops.embed_bwd(ids, dy.contiguous(), ctx.vocab, ctx.scale), None
+
+
 def zero_centred_rms_norm(x, w, eps=1e-6):
     return ZeroCentredRMSNorm.apply(x, w, eps)
 
@@ -94,3 +110,7 @@ def rms_norm(x, w, z=None, eps=1e-6, weight_offset=1.0, act=None):
 
 def layer_norm(x, w, b=None, eps=1e-5):
     return LayerNorm.apply(x, w, b, eps)
+
+
+def embedding(ids, table, scale=1.0):
+    return Embedding.apply(ids, table, scale)

@@ -475,6 +475,59 @@ def layernorm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, mean: torc
     return dx, dw, db
 
 
+def _index(name: str, t: torch.Tensor, device) -> int:
+    """The length of an int64 index vector on ``device``."""
+    if t.dim() != 1 or t.dtype != torch.int64 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int64 [tokens] tensor on {device}")
+    return int(t.shape[0])
+
+
+def embed_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, *,
+              y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = scale * table[ids[t]], rounded once; table [vocab, width], ids
+    [tokens] int64.  An id outside [0, vocab) gives a zero row."""
+    vocab, width = _rows_width(table)
+    dt = _dt(table)
+    tokens = _index("ids", ids, table.device)
+    if y is None:
+        y = torch.empty(tokens, width, dtype=table.dtype, device=table.device)
+    elif y.dtype != table.dtype or y.device != table.device or tuple(y.shape) != (tokens, width) \
+            or not y.is_contiguous():
+        raise ValueError(f"y must be a contiguous {table.dtype} [{tokens}, {width}] tensor on "
+                         f"{table.device}")
+    with torch.cuda.device(table.device):
+        check("embed_fwd", load().embed_fwd(tokens, vocab, width, scale, dt, _ptr(ids), _ptr(table),
+                                            _ptr(y), _stream(table, stream)))
+    return y
+
+
+def embed_bwd(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1.0, *,
+              dtable: Optional[torch.Tensor] = None, accumulate: bool = False,
+              ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of embed_fwd's table: dtable[v] = scale * the sum of dy[t]
+    over the tokens with ids[t] == v, [vocab, width] of dy's dtype.  With
+    accumulate, the sums are added to the given dtable."""
+    tokens, width = _rows_width(dy)
+    dt = _dt(dy)
+    if _index("ids", ids, dy.device) != tokens:
+        raise ValueError(f"ids must have dy's {tokens} tokens, got {ids.shape[0]}")
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dtable to add to")
+        dtable = torch.empty(vocab, width, dtype=dy.dtype, device=dy.device)
+    elif dtable.dtype != dy.dtype or dtable.device != dy.device \
+            or tuple(dtable.shape) != (vocab, width) or not dtable.is_contiguous():
+        raise ValueError(f"dtable must be a contiguous {dy.dtype} [{vocab}, {width}] tensor on "
+                         f"{dy.device}")
+    lib = load()
+    ws, nws = _buffer(ws, int(lib.embed_bwd_workspace_bytes(tokens, width)), dy.device)
+    with torch.cuda.device(dy.device):
+        check("embed_bwd", lib.embed_bwd(tokens, vocab, width, scale, dt, _ptr(ids), _ptr(dy),
+                                         int(accumulate), _ptr(dtable), _ptr(ws), nws,
+                                         _stream(dy, stream)))
+    return dtable
+
+
 def rn_describe(width: int, dtype=torch.bfloat16) -> str:
     """The provenance string for (width, dtype): kernels, team shape, reduction
     order, dw tree, accumulator; "unsupported" for an invalid pair."""
