@@ -403,6 +403,54 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
                     size_t ws_bytes, rn_stream stream);
 
 /*
+ * Linear cross entropy
+ * --------------------
+ * The last operator of a language model: the projection of x onto the
+ * vocabulary and the log-probability of one target token per row, without
+ * storing the logits (RL-Kernel RFC #415 lists a logit soft cap and the selected
+ * log-probability):
+ *   z = x w^T;  s = z when softcap == 0, else softcap * tanh(z / softcap)
+ *   lse[r] = log(sum_v exp(s[r, v])),  nll[r] = lse[r] - s[r, target[r]]
+ * so -nll is the target's log-probability.  A row whose target is outside
+ * [0, vocab) is ignored: its nll is 0 (lse is written) and it has no gradient.
+ * x: [rows, width] dt, read.  w: [vocab, width] dt, read (an embedding table
+ * may serve).  target: [rows] int64, read, 8-byte aligned.  nll, lse: [rows]
+ * fp32, written, one of them may be NULL.  dt is RN_BF16 or RN_F16 (the
+ * products run on the tensor cores, with fp32 accumulators); RN_F32 is
+ * RN_E_DTYPE.  0 <= rows <= 2^22, 1 <= vocab <= 2^24, softcap finite and not
+ * negative, else RN_E_ARG.
+ * A row's nll and lse are bitwise the same alone or inside any batch.
+ * ws: device workspace of ws_bytes >= linear_xent_fwd_workspace_bytes(rows,
+ * vocab) (two floats for every 256 logits), 16-byte aligned, contents
+ * irrelevant.  rows == 0 enqueues nothing.
+ */
+size_t linear_xent_fwd_workspace_bytes(int64_t rows, int64_t vocab);
+rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype dt, const void* x,
+                          const void* w, const int64_t* target, float softcap, float* nll, float* lse,
+                          void* ws, size_t ws_bytes, rn_stream stream);
+
+/*
+ * Linear cross entropy backward, the gradient of sum_r dnll[r] * nll[r]:
+ *   dz[r, v] = dnll[r] * (exp(s[r, v] - lse[r]) - [v == target[r]]) * ds/dz
+ *   dx = dz w,  dw = dz^T x
+ * lse: [rows] fp32 from linear_xent_fwd with the same softcap, read.  dnll:
+ * [rows] fp32, read.  dx: [rows, width] dt, written, or NULL.  dw: [vocab,
+ * width] dt, written (every row), or NULL; one of them is given.
+ * The logits are computed again, a piece of the vocabulary at a time; dz is
+ * rounded once to dt (for RN_F16 scaled by a power of two taken from the
+ * largest |dnll|, which the products undo) as an operand of the tensor cores.
+ * Ignored rows take no part, whatever x, lse and dnll hold there; their rows of
+ * dx are zero.  A row's dx is bitwise the same alone or inside any batch of the
+ * same largest |dnll| (RN_BF16: any batch); dw is bitwise the same across runs.
+ * ws: device workspace of ws_bytes >= linear_xent_bwd_workspace_bytes(rows,
+ * width, vocab), 16-byte aligned, contents irrelevant.
+ */
+size_t linear_xent_bwd_workspace_bytes(int64_t rows, int32_t width, int64_t vocab);
+rn_status linear_xent_bwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype dt, const void* x,
+                          const void* w, const int64_t* target, const float* lse, const float* dnll,
+                          float softcap, void* dx, void* dw, void* ws, size_t ws_bytes, rn_stream stream);
+
+/*
  * Provenance record (RFC #415 section 4, point 8): a static, NUL-terminated
  * string naming the kernels, the reduction schedule and tree, and the
  * accumulator for (width, dt); "unsupported" for an invalid pair.  The

@@ -14,6 +14,8 @@ from .ops import (  # noqa: F401
     gated_norm_fwd,
     layernorm_bwd,
     layernorm_fwd,
+    linear_xent_bwd,
+    linear_xent_fwd,
     norm_bwd,
     norm_bwd_workspace_bytes,
     norm_fwd,

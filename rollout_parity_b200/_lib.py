@@ -78,6 +78,12 @@ SIGNATURES = {
     "embed_bwd_workspace_bytes": (c_sz, [c_i64, c_i32]),
     "embed_bwd": (c_i32, [c_i64, c_i64, c_i32, c_f32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_sz,
                           c_vp]),
+    "linear_xent_fwd_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "linear_xent_fwd": (c_i32, [c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_f32, c_vp, c_vp,
+                                c_vp, c_sz, c_vp]),
+    "linear_xent_bwd_workspace_bytes": (c_sz, [c_i64, c_i32, c_i64]),
+    "linear_xent_bwd": (c_i32, [c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_f32,
+                                c_vp, c_vp, c_vp, c_sz, c_vp]),
     "rn_describe": (ctypes.c_char_p, [c_i32, c_i32]),
     "rn_bwd_launches": (c_i32, [c_i64, c_i32, c_i32]),
     "rn_status_string": (ctypes.c_char_p, [c_i32]),

@@ -96,6 +96,27 @@ class Embedding(torch.autograd.Function):
         return None, ops.embed_bwd(ids, dy.contiguous(), ctx.vocab, ctx.scale), None
 
 
+class LinearCrossEntropy(torch.autograd.Function):
+    """nll[r] = -log softmax(s)[target[r]], s = x w^T (softcap 0) or softcap *
+    tanh(x w^T / softcap); x [rows, width], w [vocab, width] bf16/fp16, target
+    [rows] int64 (outside [0, vocab): ignored)."""
+
+    @staticmethod
+    def forward(ctx, x, w, target, softcap=0.0):
+        nll, lse = ops.linear_xent_fwd(x, w, target, softcap)
+        ctx.save_for_backward(x, w, target, lse)
+        ctx.softcap = softcap
+        return nll
+
+    @staticmethod
+    def backward(ctx, dnll):
+        x, w, target, lse = ctx.saved_tensors
+        want_dx, want_dw = ctx.needs_input_grad[:2]
+        dx, dw = ops.linear_xent_bwd(x, w, target, lse, dnll.contiguous(), ctx.softcap,
+                                     want_dx=want_dx, want_dw=want_dw)
+        return dx, dw, None, None
+
+
 def zero_centred_rms_norm(x, w, eps=1e-6):
     return ZeroCentredRMSNorm.apply(x, w, eps)
 
@@ -114,3 +135,7 @@ def layer_norm(x, w, b=None, eps=1e-5):
 
 def embedding(ids, table, scale=1.0):
     return Embedding.apply(ids, table, scale)
+
+
+def linear_cross_entropy(x, w, target, softcap=0.0):
+    return LinearCrossEntropy.apply(x, w, target, softcap)

@@ -528,6 +528,69 @@ def embed_bwd(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1.
     return dtable
 
 
+def _head(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor) -> Tuple[int, int, int]:
+    """(rows, width, vocab) of a projection x [rows, width] onto w [vocab, width]."""
+    rows, width = _rows_width(x)
+    if w.dim() != 2 or w.dtype != x.dtype or w.device != x.device or int(w.shape[1]) != width \
+            or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {x.dtype} [vocab, {width}] tensor on {x.device}")
+    if _index("target", target, x.device) != rows:
+        raise ValueError(f"target must have x's {rows} rows, got {target.shape[0]}")
+    return rows, width, int(w.shape[0])
+
+
+def linear_xent_fwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, softcap: float = 0.0, *,
+                    nll: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """The negative log-probability of one target token per row under the
+    softmax of x w^T (with softcap > 0, of softcap * tanh(x w^T / softcap)),
+    and the log of the softmax's sum.  x [rows, width] and w [vocab, width]
+    bf16 or fp16, target [rows] int64 (outside [0, vocab): ignored, nll 0).
+    Returns (nll, lse), fp32 [rows]."""
+    rows, width, vocab = _head(x, w, target)
+    dt = _dt(x)
+    nll = torch.empty(rows, dtype=torch.float32, device=x.device) if nll is None else \
+        _vec("nll", nll, rows, x.device)
+    lse = torch.empty(rows, dtype=torch.float32, device=x.device) if lse is None else \
+        _vec("lse", lse, rows, x.device)
+    lib = load()
+    ws, nws = _buffer(ws, int(lib.linear_xent_fwd_workspace_bytes(rows, vocab)), x.device)
+    with torch.cuda.device(x.device):
+        check("linear_xent_fwd",
+              lib.linear_xent_fwd(rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target), softcap,
+                                  _ptr(nll), _ptr(lse), _ptr(ws), nws, _stream(x, stream)))
+    return nll, lse
+
+
+def linear_xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                    dnll: torch.Tensor, softcap: float = 0.0, *, want_dx: bool = True,
+                    want_dw: bool = True, dx: Optional[torch.Tensor] = None,
+                    dw: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None):
+    """The gradient of sum(dnll * nll) of linear_xent_fwd (lse from that call).
+    Returns (dx, dw) of x's dtype, None for the one not wanted."""
+    rows, width, vocab = _head(x, w, target)
+    dt = _dt(x)
+    _vec("lse", lse, rows, x.device)
+    _vec("dnll", dnll, rows, x.device)
+    if dx is not None:
+        _mat("dx", dx, x)
+    elif want_dx:
+        dx = torch.empty_like(x)
+    if dw is not None:
+        _mat("dw", dw, w)
+    elif want_dw:
+        dw = torch.empty_like(w)
+    lib = load()
+    ws, nws = _buffer(ws, int(lib.linear_xent_bwd_workspace_bytes(rows, width, vocab)), x.device)
+    with torch.cuda.device(x.device):
+        check("linear_xent_bwd",
+              lib.linear_xent_bwd(rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
+                                  _ptr(dnll), softcap, _ptr(dx), _ptr(dw), _ptr(ws), nws,
+                                  _stream(x, stream)))
+    return dx, dw
+
+
 def rn_describe(width: int, dtype=torch.bfloat16) -> str:
     """The provenance string for (width, dtype): kernels, team shape, reduction
     order, dw tree, accumulator; "unsupported" for an invalid pair."""
