@@ -10,12 +10,11 @@ using namespace rn_detail;
 namespace {
 
 // dw and db from the CTAs' partials, n rows of each: the level-by-level
-// pairwise tree, one CTA of 8 warps per 32 columns.  Warp w streams the aligned
-// block of L rows [wL, (w+1)L), a perfect subtree, through the binary counter;
-// the warps' results are joined by the tree in shared memory.
-constexpr int kLnFoldWarps = 8;
-template <int LB>
-__global__ void __launch_bounds__(32 * kLnFoldWarps)
+// pairwise tree, one CTA of W warps per 32 columns.  Warp w streams the aligned
+// block of L rows [wL, (w+1)L), a perfect subtree, all of them in flight; the
+// warps' results are joined by the tree in shared memory.
+template <int LB, int W>
+__global__ void __launch_bounds__(32 * W)
 k_ln_fold(const float* __restrict__ pw, const float* __restrict__ pb, int n, int H,
           float* __restrict__ dw, float* __restrict__ db) {
   constexpr int L = 1 << LB;
@@ -26,25 +25,26 @@ k_ln_fold(const float* __restrict__ pw, const float* __restrict__ pb, int n, int
   float* out = blockIdx.y == 0 ? dw : db;
   const int c = blockIdx.x * 32 + lane;
   const int start = wid * L;
-  const int cnt = n - start <= 0 ? 0 : (n - start < L ? n - start : L);
+  const int cnt = c >= H || n <= start ? 0 : (n - start < L ? n - start : L);
+  float v[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) v[i] = i < cnt ? __ldcg(in + int64_t(start + i) * H + c) : 0.0f;
   TreeCounter<LB, float> tc;
-  if (c < H) {
-#pragma unroll 16
-    for (int i = 0; i < L; ++i)
-      if (i < cnt) tc.push(i, __ldcg(in + int64_t(start + i) * H + c));
-  }
-  __shared__ float sm[kLnFoldWarps][32];
-  sm[wid][lane] = cnt > 0 && c < H ? tc.finish(cnt) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < L; ++i)
+    if (i < cnt) tc.push(i, v[i]);
+  __shared__ float sm[W][32];
+  sm[wid][lane] = cnt > 0 ? tc.finish(cnt) : 0.0f;
   __syncthreads();
   if (wid == 0 && c < H) {
     const int nw = (n + L - 1) / L;
-    float p[kLnFoldWarps];
+    float p[W];
 #pragma unroll
-    for (int i = 0; i < kLnFoldWarps; ++i) p[i] = sm[i][lane];
+    for (int i = 0; i < W; ++i) p[i] = sm[i][lane];
 #pragma unroll
-    for (int s = 1; s < kLnFoldWarps; s <<= 1) {
+    for (int s = 1; s < W; s <<= 1) {
 #pragma unroll
-      for (int l = 0; l + s < kLnFoldWarps; l += 2 * s)
+      for (int l = 0; l + s < W; l += 2 * s)
         if (l + s < nw) p[l] = __fadd_rn(p[l], p[l + s]);
     }
     out[c] = p[0];
@@ -60,10 +60,11 @@ struct LnPlan {
 
 LnPlan ln_plan(int64_t rows, int32_t width, rn_dtype dt) {
   LnPlan p;
-  p.s = row_sched(width, dt);
-  p.block_rows = dt == RN_F32    ? ln_bwd_block_rows<RN_F32>(p.s, rows)
-                 : dt == RN_BF16 ? ln_bwd_block_rows<RN_BF16>(p.s, rows)
-                                 : ln_bwd_block_rows<RN_F16>(p.s, rows);
+  p.s = ln_bwd_sched(width, dt);
+  const bool wide = width / vec_elems(dt) > 128;
+  p.block_rows = dt == RN_F32    ? ln_bwd_block_rows<RN_F32>(p.s, rows, wide)
+                 : dt == RN_BF16 ? ln_bwd_block_rows<RN_BF16>(p.s, rows, wide)
+                                 : ln_bwd_block_rows<RN_F16>(p.s, rows, wide);
   p.ctas = int((rows + p.block_rows - 1) / p.block_rows);
   return p;
 }
@@ -76,10 +77,11 @@ size_t ln_ws_bytes(int64_t rows, int32_t width, rn_dtype dt) {
 
 rn_status launch_ln_fold(const float* pw, const float* pb, int n, int H, float* dw, float* db,
                          cudaStream_t st) {
-  const dim3 grid((H + 31) / 32, db ? 2 : 1), block(32 * kLnFoldWarps);
-  if (n <= 8 * kLnFoldWarps) return launch_pdl(k_ln_fold<3>, grid, block, 0, st, pw, pb, n, H, dw, db);
-  if (n <= 32 * kLnFoldWarps) return launch_pdl(k_ln_fold<5>, grid, block, 0, st, pw, pb, n, H, dw, db);
-  if (n <= 128 * kLnFoldWarps) return launch_pdl(k_ln_fold<7>, grid, block, 0, st, pw, pb, n, H, dw, db);
+  const dim3 grid((H + 31) / 32, db ? 2 : 1);
+  if (n <= 64) return launch_pdl(k_ln_fold<3, 8>, grid, dim3(256), 0, st, pw, pb, n, H, dw, db);
+  if (n <= 256) return launch_pdl(k_ln_fold<3, 32>, grid, dim3(1024), 0, st, pw, pb, n, H, dw, db);
+  if (n <= 512) return launch_pdl(k_ln_fold<4, 32>, grid, dim3(1024), 0, st, pw, pb, n, H, dw, db);
+  if (n <= 1024) return launch_pdl(k_ln_fold<5, 32>, grid, dim3(1024), 0, st, pw, pb, n, H, dw, db);
   return RN_E_ARG;   // unreachable: at most 592 CTAs
 }
 
@@ -159,9 +161,9 @@ rn_status layernorm_bwd(int64_t rows, int32_t width, rn_dtype dt, const void* x,
                     static_cast<const uint4*>(dy), mean, rstd, row_mask, static_cast<uint4*>(dx),
                     pw, pb};
   switch (dt) {
-    case RN_BF16: e = launch_ln_bwd<RN_BF16>(p.s, a, p.block_rows, p.ctas, st); break;
-    case RN_F16: e = launch_ln_bwd<RN_F16>(p.s, a, p.block_rows, p.ctas, st); break;
-    default: e = launch_ln_bwd<RN_F32>(p.s, a, p.block_rows, p.ctas, st); break;
+    case RN_BF16: e = launch_ln_bwd<RN_BF16>(p.s, a, p.ctas, st); break;
+    case RN_F16: e = launch_ln_bwd<RN_F16>(p.s, a, p.ctas, st); break;
+    default: e = launch_ln_bwd<RN_F32>(p.s, a, p.ctas, st); break;
   }
   if (e != RN_OK || p.ctas == 1) return e;
   return launch_ln_fold(pw, pb, p.ctas, width, dw, db, st);

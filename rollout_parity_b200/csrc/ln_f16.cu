@@ -4,6 +4,6 @@
 
 namespace rn_detail {
 template rn_status launch_ln_fwd<RN_F16>(const Sched&, const LnFwdArgs&, cudaStream_t);
-template int64_t ln_bwd_block_rows<RN_F16>(const Sched&, int64_t);
-template rn_status launch_ln_bwd<RN_F16>(const Sched&, const LnBwdArgs&, int64_t, int, cudaStream_t);
+template int64_t ln_bwd_block_rows<RN_F16>(const Sched&, int64_t, bool);
+template rn_status launch_ln_bwd<RN_F16>(const Sched&, const LnBwdArgs&, int, cudaStream_t);
 }  // namespace rn_detail

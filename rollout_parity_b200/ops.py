@@ -81,6 +81,21 @@ def _stream(x: torch.Tensor, stream) -> int:
     return s.cuda_stream
 
 
+def _launch(name: str, x: torch.Tensor, stream, *args) -> None:
+    """Calls the C entry point ``name`` on x's device (made current only when it
+    is not: the context manager costs more than a small call's checks) and on
+    ``stream``, or that device's current stream when None."""
+    fn = getattr(load(), name)
+    index = x.device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(x, stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    check(name, status)
+
+
 def norm_bwd_workspace_bytes(rows: int, width: int) -> int:
     return int(load().norm_bwd_workspace_bytes(rows, width))
 
@@ -407,10 +422,22 @@ def _row_mask(row_mask: Optional[torch.Tensor], rows: int, device) -> Optional[t
     return row_mask.view(torch.uint8)
 
 
-def _buffer(ws: Optional[torch.Tensor], need: int, device) -> Tuple[torch.Tensor, int]:
-    """A workspace of at least ``need`` bytes (the caller's is passed through)."""
+def _buffer(ws: Optional[torch.Tensor], need: int, device,
+            stream) -> Tuple[Optional[torch.Tensor], int]:
+    """A workspace of at least ``need`` bytes (the caller's is passed through;
+    none when none is needed).  It is allocated on the stream that uses it, so
+    that the caching allocator does not give it to another stream's work while
+    the call still runs."""
     if ws is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device), max(need, 16)
+        if not need:
+            return None, 0
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device) if stream else \
+                torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=device), need
     if ws.device != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous buffer on the tensors' device")
     return ws, ws.numel() * ws.element_size()
@@ -436,10 +463,8 @@ def layernorm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor] = 
         _vec("mean", mean, rows, x.device)
     if rstd is not None:
         _vec("rstd", rstd, rows, x.device)
-    with torch.cuda.device(x.device):
-        check("layernorm_fwd",
-              load().layernorm_fwd(rows, width, eps, dt, _ptr(x), _ptr(w), _ptr(b), _ptr(y),
-                                   _ptr(mean), _ptr(rstd), _stream(x, stream)))
+    _launch("layernorm_fwd", x, stream, rows, width, eps, dt, _ptr(x), _ptr(w), _ptr(b), _ptr(y),
+            _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
@@ -466,12 +491,10 @@ def layernorm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, mean: torc
     elif want_db:
         db = torch.empty(width, dtype=torch.float32, device=x.device)
     lib = load()
-    ws, nws = _buffer(ws, int(lib.layernorm_bwd_workspace_bytes(rows, width, dt)), x.device)
-    with torch.cuda.device(x.device):
-        check("layernorm_bwd",
-              lib.layernorm_bwd(rows, width, dt, _ptr(x), _ptr(w), _ptr(dy), _ptr(mean),
-                                _ptr(rstd), _ptr(row_mask), _ptr(dx), _ptr(dw), _ptr(db),
-                                _ptr(ws), nws, _stream(x, stream)))
+    ws, nws = _buffer(ws, int(lib.layernorm_bwd_workspace_bytes(rows, width, dt)), x.device,
+                      stream)
+    _launch("layernorm_bwd", x, stream, rows, width, dt, _ptr(x), _ptr(w), _ptr(dy), _ptr(mean),
+            _ptr(rstd), _ptr(row_mask), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nws)
     return dx, dw, db
 
 
@@ -495,9 +518,8 @@ def embed_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, *,
             or not y.is_contiguous():
         raise ValueError(f"y must be a contiguous {table.dtype} [{tokens}, {width}] tensor on "
                          f"{table.device}")
-    with torch.cuda.device(table.device):
-        check("embed_fwd", load().embed_fwd(tokens, vocab, width, scale, dt, _ptr(ids), _ptr(table),
-                                            _ptr(y), _stream(table, stream)))
+    _launch("embed_fwd", table, stream, tokens, vocab, width, scale, dt, _ptr(ids), _ptr(table),
+            _ptr(y))
     return y
 
 
@@ -520,11 +542,10 @@ def embed_bwd(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1.
         raise ValueError(f"dtable must be a contiguous {dy.dtype} [{vocab}, {width}] tensor on "
                          f"{dy.device}")
     lib = load()
-    ws, nws = _buffer(ws, int(lib.embed_bwd_workspace_bytes(tokens, width)), dy.device)
-    with torch.cuda.device(dy.device):
-        check("embed_bwd", lib.embed_bwd(tokens, vocab, width, scale, dt, _ptr(ids), _ptr(dy),
-                                         int(accumulate), _ptr(dtable), _ptr(ws), nws,
-                                         _stream(dy, stream)))
+    ws, nws = _buffer(ws, int(lib.embed_bwd_workspace_bytes(tokens, width)), dy.device,
+                      stream)
+    _launch("embed_bwd", dy, stream, tokens, vocab, width, scale, dt, _ptr(ids), _ptr(dy),
+            int(accumulate), _ptr(dtable), _ptr(ws), nws)
     return dtable
 
 
@@ -554,11 +575,10 @@ def linear_xent_fwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, soft
     lse = torch.empty(rows, dtype=torch.float32, device=x.device) if lse is None else \
         _vec("lse", lse, rows, x.device)
     lib = load()
-    ws, nws = _buffer(ws, int(lib.linear_xent_fwd_workspace_bytes(rows, vocab)), x.device)
-    with torch.cuda.device(x.device):
-        check("linear_xent_fwd",
-              lib.linear_xent_fwd(rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target), softcap,
-                                  _ptr(nll), _ptr(lse), _ptr(ws), nws, _stream(x, stream)))
+    ws, nws = _buffer(ws, int(lib.linear_xent_fwd_workspace_bytes(rows, vocab)), x.device,
+                      stream)
+    _launch("linear_xent_fwd", x, stream, rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target),
+            softcap, _ptr(nll), _ptr(lse), _ptr(ws), nws)
     return nll, lse
 
 
@@ -582,12 +602,10 @@ def linear_xent_bwd(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, lse:
     elif want_dw:
         dw = torch.empty_like(w)
     lib = load()
-    ws, nws = _buffer(ws, int(lib.linear_xent_bwd_workspace_bytes(rows, width, vocab)), x.device)
-    with torch.cuda.device(x.device):
-        check("linear_xent_bwd",
-              lib.linear_xent_bwd(rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target), _ptr(lse),
-                                  _ptr(dnll), softcap, _ptr(dx), _ptr(dw), _ptr(ws), nws,
-                                  _stream(x, stream)))
+    ws, nws = _buffer(ws, int(lib.linear_xent_bwd_workspace_bytes(rows, width, vocab)), x.device,
+                      stream)
+    _launch("linear_xent_bwd", x, stream, rows, width, vocab, dt, _ptr(x), _ptr(w), _ptr(target),
+            _ptr(lse), _ptr(dnll), softcap, _ptr(dx), _ptr(dw), _ptr(ws), nws)
     return dx, dw
 
 

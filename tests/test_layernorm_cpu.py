@@ -74,8 +74,8 @@ def test_workspace_sizes(lib):
     ws = lib.layernorm_bwd_workspace_bytes
     assert ws(0, H, DType.BF16) == 0 and ws(-1, H, DType.BF16) == 0
     assert ws(ROWS, 12, DType.BF16) == 0 and ws(ROWS, H, 9) == 0
-    # at most four CTAs an SM write partials, however many rows
-    assert ws(1 << 36, H, DType.BF16) <= 592 * H * 8
+    # a bounded number of CTAs writes partials, however many rows
+    assert ws(1 << 36, H, DType.BF16) <= 740 * H * 8
 
 
 def test_formulas_match_differences():
