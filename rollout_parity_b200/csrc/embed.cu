@@ -76,12 +76,12 @@ k_embed_fwd(int64_t tokens, int64_t vocab, int nv, float scale, const int64_t* _
 struct EmbedWs {
   uint32_t* key[2];      // [tokens] sorted ids (vocab: no row), ping and pong
   uint32_t* tok[2];      // [tokens] their tokens
-  uint32_t* run_start;   // [tokens + 1] first position of each run
-  uint32_t* run_of;      // [tokens/32 + 1] the run that holds position 32 e
-  uint32_t* counts;      // [0] runs, [1] runs longer than a leaf
-  uint32_t* long_runs;   // [tokens/32 + 1] those runs, in any order
-  float* first_leaf;     // [tokens/32 + 1][H] leaf 0 of the run starting at s: row s/32
-  float* more_leaves;    // [tokens/32 + 1][H] leaf j > 0: row ceil(s/32) + j - 1
+  uint32_t* long_count;  // runs longer than a leaf
+  uint32_t* long_runs;   // [tokens/32 + 1] their first positions, in any order
+  // sums of the long runs' leaves: of the leaf that starts at position p, row p/32
+  // (32 positions hold at most one first leaf of a long run and one later leaf)
+  float* first_leaf;     // [tokens/32 + 1][H]
+  float* more_leaves;    // [tokens/32 + 1][H]
   size_t bytes;
 };
 
@@ -99,9 +99,7 @@ EmbedWs embed_ws(void* base, int64_t tokens, int width) {
     w.key[i] = reinterpret_cast<uint32_t*>(take(n * 4));
     w.tok[i] = reinterpret_cast<uint32_t*>(take(n * 4));
   }
-  w.run_start = reinterpret_cast<uint32_t*>(take((n + 1) * 4));
-  w.run_of = reinterpret_cast<uint32_t*>(take(b * 4));
-  w.counts = reinterpret_cast<uint32_t*>(take(8));
+  w.long_count = reinterpret_cast<uint32_t*>(take(4));
   w.long_runs = reinterpret_cast<uint32_t*>(take(b * 4));
   w.first_leaf = reinterpret_cast<float*>(take(b * size_t(width) * 4));
   w.more_leaves = reinterpret_cast<float*>(take(b * size_t(width) * 4));
@@ -111,7 +109,7 @@ EmbedWs embed_ws(void* base, int64_t tokens, int width) {
 
 // ---------------------------------------------------------------------------
 // gradient, pass 1: cluster 0 sorts the tokens by id (stable least-significant-
-// digit radix sort) and lists the runs; the other clusters clear dE meanwhile.
+// digit radix sort); the other clusters clear dE meanwhile.
 // A warp owns a contiguous piece of the positions.  Per pass: a histogram of
 // each warp's piece, prefix sums over the warps, the cluster's CTAs
 // (distributed shared memory) and the bins, then the scatter in order.
@@ -122,6 +120,20 @@ struct SortShared {
   uint32_t base[1 << kDigitBits];
   uint32_t warp_sum[kSortWarps];
 };
+
+constexpr int kAhead = 4;   // groups of 32 keys a warp has in flight
+
+// The lanes whose digit equals this lane's, among those that are `in`.
+__device__ __forceinline__ unsigned same_digit(uint32_t d, bool in) {
+  unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+  for (int b = 0; b < kDigitBits; ++b) {
+    const bool bit = d & (1u << b);
+    const unsigned m = __ballot_sync(0xffffffffu, bit);
+    same &= bit ? m : ~m;
+  }
+  return same;
+}
 
 // exclusive prefix sum over the CTA's threads; every thread must call it
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* warp_sum, uint32_t* all) {
@@ -153,6 +165,7 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
   SortShared& sm = *reinterpret_cast<SortShared*>(smem_raw);
   griddep_trigger();
   griddep_wait();
+  cg::cluster_group cluster = cg::this_cluster();
   if (blockIdx.x >= kSortCtas) {
     const int64_t stride = int64_t(gridDim.x - kSortCtas) * kSortThreads;
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -161,7 +174,6 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
       clear[i] = zero;
     return;
   }
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const unsigned below = (1u << lane) - 1u;
   // this warp's positions: a multiple of 32 each, in order of (CTA, warp)
@@ -185,12 +197,16 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
     };
     for (int i = tid; i < kSortWarps * (1 << kDigitBits); i += kSortThreads) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
-    for (uint32_t p = lo; p < hi; p += 32) {
-      const bool in = p + lane < hi;
-      const uint32_t d = in ? (key_at(p + lane) >> shift) & (bins - 1) : 0xffffffffu;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (in && (same & below) == 0) sm.hist[w][d] += __popc(same);
-      __syncwarp();
+    for (uint32_t p0 = lo; p0 < hi; p0 += 32 * kAhead) {
+      uint32_t k[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) k[i] = p0 + 32 * i + lane < hi ? key_at(p0 + 32 * i + lane) : 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (p0 + 32 * i >= hi) break;   // uniform
+        const bool in = p0 + 32 * i + lane < hi;
+        if (in) atomicAdd(&sm.hist[w][(k[i] >> shift) & (bins - 1)], 1u);   // (a count: no order)
+      }
     }
     __syncthreads();
     uint32_t mine = 0;
@@ -217,161 +233,180 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
     const uint32_t start = block_prefix(all, sm.warp_sum, &sum);   // over the bins
     if (tid < bins) sm.base[tid] = start + before;
     __syncthreads();
-    for (uint32_t p = lo; p < hi; p += 32) {
-      const bool in = p + lane < hi;
-      const uint32_t key = in ? key_at(p + lane) : 0;
-      const uint32_t d = in ? (key >> shift) & (bins - 1) : 0xffffffffu;
-      const uint32_t t = !in ? 0 : pass > 0 ? __ldcg(src_tok + p + lane) : p + lane;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (in) {
-        const uint32_t at = sm.base[d] + sm.hist[w][d] + __popc(same & below);
-        __stcg(dst_key + at, key);
-        __stcg(dst_tok + at, t);
+    for (uint32_t p0 = lo; p0 < hi; p0 += 32 * kAhead) {
+      uint32_t k[kAhead], t[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const uint32_t p = p0 + 32 * i + lane;
+        k[i] = p < hi ? key_at(p) : 0;
+        t[i] = p < hi && pass > 0 ? __ldcg(src_tok + p) : p;
       }
-      __syncwarp();
-      if (in && (same & below) == 0) sm.hist[w][d] += __popc(same);
-      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (p0 + 32 * i >= hi) break;   // uniform
+        const bool in = p0 + 32 * i + lane < hi;
+        const uint32_t d = (k[i] >> shift) & (bins - 1);
+        const unsigned same = same_digit(d, in);
+        if (in) {
+          const uint32_t at = sm.base[d] + sm.hist[w][d] + __popc(same & below);
+          __stcg(dst_key + at, k[i]);
+          __stcg(dst_tok + at, t[i]);
+        }
+        __syncwarp();
+        if (in && (same & below) == 0) sm.hist[w][d] += __popc(same);
+        __syncwarp();
+      }
     }
-    __threadfence();
-    cluster.sync();   // the scatter is complete; the totals may be overwritten
+    // the scatter is complete (the barrier releases this thread's stores to the
+    // cluster and acquires the others'), and the totals may be overwritten
+    cluster.sync();
   }
 
-  // the runs: positions whose id differs from the one before
-  const uint32_t* key = ws.key[(passes + 1) & 1];
-  auto starts = [&](uint32_t p) -> unsigned {   // one bit a position of [p, p + 32)
-    const bool in = p + lane < hi;
-    bool s = false;
-    if (in) s = p + lane == 0 || __ldcg(key + p + lane) != __ldcg(key + p + lane - 1);
-    return __ballot_sync(0xffffffffu, s);
-  };
-  uint32_t n = 0;
-  for (uint32_t p = lo; p < hi; p += 32) n += __popc(starts(p));
-  // prefix over the CTA's warps (a warp's count is carried by its lane 0)
-  uint32_t cta_runs;
-  uint32_t at = block_prefix(lane == 0 ? n : 0, sm.warp_sum, &cta_runs);
-  at = __shfl_sync(0xffffffffu, at, 0);
-  if (tid == 0) sm.total[0] = cta_runs;
-  cluster.sync();
-  uint32_t all = 0;
-  for (int c = 0; c < kSortCtas; ++c) {
-    const uint32_t m = *cluster.map_shared_rank(&sm.total[0], c);
-    if (c < int(blockIdx.x)) at += m;
-    all += m;
-  }
-  for (uint32_t p = lo; p < hi; p += 32) {
-    const unsigned s = starts(p);
-    if ((s >> lane) & 1u) ws.run_start[at + __popc(s & below)] = p + lane;
-    if (lane == 0) ws.run_of[p / 32] = at + (s & 1u) - 1;   // the run that holds position p
-    at += __popc(s);
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    ws.run_start[all] = tokens;
-    ws.counts[0] = all;
-    ws.counts[1] = 0;
-  }
-  cluster.sync();   // no CTA leaves while another reads its shared memory
+  if (blockIdx.x == 0 && tid == 0) *ws.long_count = 0;
 }
 
 // ---------------------------------------------------------------------------
-// gradient, pass 2: sums of the leaves.  A unit is one leaf and one slab of
-// columns (two 16-byte vectors a lane, 1 KB of a row); a warp takes units in
-// turn and has the tokens' rows of four steps in flight.  The unit of run u
-// sums its leaf 0; leaf j > 0 of a run is summed by the unit of the j-th
-// multiple of 32 among the run's positions (there are at least as many as
-// leaves after the first).  A run of one leaf is written to dE at once.
+// gradient, pass 2: sums of the leaves.  A warp takes 32 sorted positions and
+// 512 bytes of their columns (16 a lane), and sums the leaves that start among
+// them; the last one may reach up to 31 positions further.  The tokens' rows
+// are read eight at a time, across the ends of runs: most runs have one or two
+// tokens, and a warp to a run had too few bytes in flight (32768 tokens of 4 KB
+// rows: 95 us).  A run of one leaf is written to dE at once.
 // ---------------------------------------------------------------------------
-template <int DT>
-__device__ __forceinline__ void embed_store(uint4* at, const float2 (&s)[Fmt<DT>::VE / 2],
-                                            float scale, bool add) {
+// The first position of [lo, hi] whose key is at least k, one warp (key[hi] is, or
+// hi is one past the last position): 32 probes a step.
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t* key, uint32_t tokens, uint32_t lo, uint32_t hi,
+                                                uint32_t k) {
+  const uint32_t lane = threadIdx.x & 31;
+  while (lo < hi) {   // uniform
+    const uint32_t step = (hi - lo) / 32 + 1;
+    const uint32_t at = min(lo + lane * step, hi);
+    const unsigned b = __ballot_sync(0xffffffffu, at >= tokens || __ldcg(key + at) >= k);
+    if (b & 1u) return lo;
+    const uint32_t f = b ? __ffs(b) - 1 : 32;
+    hi = min(lo + f * step, hi);
+    lo = lo + (f - 1) * step + 1;
+  }
+  return lo;
+}
+
+// *at = fmt(scale * s), or with ADD fmt(old + scale * s)
+template <int DT, bool ADD>
+__device__ __forceinline__ void embed_store(uint4* at, const uint4& old, const float2 (&s)[Fmt<DT>::VE / 2],
+                                            float scale) {
   using F = Fmt<DT>;
   float2 f[F::VE / 2];
-  if (add) {
-    F::unpack2(*at, f);
+  if constexpr (ADD) F::unpack2(old, f);
 #pragma unroll
-    for (int q = 0; q < F::VE / 2; ++q) f[q] = fma2(s[q], bc2(scale), f[q]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < F::VE / 2; ++q) f[q] = mul2(s[q], bc2(scale));
-  }
+  for (int q = 0; q < F::VE / 2; ++q) f[q] = ADD ? fma2(s[q], bc2(scale), f[q]) : mul2(s[q], bc2(scale));
   *at = F::pack2v(f);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256)
-k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int add, int last,
-               EmbedWs ws, const uint4* __restrict__ dy, uint4* __restrict__ out) {
+template <int DT, bool ADD>
+__global__ void __launch_bounds__(256, 3)
+k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, EmbedWs ws,
+               const uint4* __restrict__ dy, uint4* __restrict__ out) {
   using F = Fmt<DT>;
-  constexpr int VE = F::VE, C = 2, U = 4;   // vectors a lane, tokens in flight
+  constexpr int VE = F::VE, U = ADD ? 4 : 8;   // tokens (and with ADD, old rows) in flight
+  constexpr uint32_t kNone = 0xffffffffu;
+  enum { kSkip = 0, kWhole = 1, kFirst = 2, kMore = 3 };   // where a leaf's sum goes
   griddep_trigger();
   griddep_wait();
   const uint32_t* key = ws.key[last];
   const uint32_t* tok = ws.tok[last];
   const int lane = threadIdx.x & 31;
-  const uint32_t slabs = (nv + 32 * C - 1) / (32 * C);
-  const uint32_t blocks = (tokens + kLeaf - 1) / kLeaf;
-  const uint64_t units = uint64_t(blocks + __ldcg(ws.counts)) * slabs;
-  const uint64_t stride = uint64_t(gridDim.x) * (blockDim.x / 32);
-  for (uint64_t u = uint64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); u < units;
-       u += stride) {
-    const uint32_t unit = uint32_t(u / slabs), slab = uint32_t(u % slabs);
-    const bool first = unit >= blocks;
-    const uint32_t run = first ? unit - blocks : __ldcg(ws.run_of + unit);
-    const uint32_t s = __ldcg(ws.run_start + run), e = __ldcg(ws.run_start + run + 1);
-    const uint32_t e0 = (s + kLeaf - 1) / kLeaf;          // the run's first multiple of 32
-    const uint32_t leaf = first ? 0 : unit - e0 + 1;      // (unit >= e0: 32 unit is in the run)
-    const uint32_t p0 = s + leaf * kLeaf;
-    if (p0 >= e) continue;                                // no such leaf
-    const uint32_t id = __ldcg(key + s);
-    if (id >= vocab) continue;                            // tokens of no row
-    const int cnt = e - p0 < kLeaf ? int(e - p0) : kLeaf;
-    const uint32_t my_tok = lane < cnt ? __ldcg(tok + p0 + lane) : 0;
-    const int v0 = int(slab) * 32 * C + lane;
-    float2 acc[C][VE / 2];
+  const uint32_t slabs = (nv + 31) / 32;
+  const uint64_t unit = uint64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const uint32_t block = uint32_t(unit / slabs), slab = uint32_t(unit % slabs);
+  const uint32_t p0 = block * 32;
+  if (p0 >= tokens) return;
+  const int v = int(slab) * 32 + lane;
+  const bool col = v < nv;
+
+  // positions p0 + lane and p0 + 32 + lane
+  const uint32_t a0 = p0 + lane, a1 = a0 + 32;
+  const uint32_t k0 = a0 < tokens ? __ldcg(key + a0) : kNone, k1 = a1 < tokens ? __ldcg(key + a1) : kNone;
+  const uint32_t t0 = a0 < tokens ? __ldcg(tok + a0) : 0, t1 = a1 < tokens ? __ldcg(tok + a1) : 0;
+  const uint32_t before = p0 > 0 ? __ldcg(key + p0 - 1) : kNone;
+  // the start of position p0's run: p0 itself, or where its key first stands
+  const uint32_t key0 = __shfl_sync(0xffffffffu, k0, 0);
+  const uint32_t start0 = key0 == before ? lower_bound(key, tokens, 0, p0, key0) : p0;
+  const uint32_t up = __shfl_up_sync(0xffffffffu, k0, 1);
+  const bool valid = a0 < tokens;
+  const unsigned upto = 0xffffffffu >> (31 - lane);         // lanes 0..lane
+  const unsigned changes = __ballot_sync(0xffffffffu, valid && k0 != (lane == 0 ? before : up));
+  const uint32_t start = changes & upto ? p0 + 31 - __clz(changes & upto) : start0;   // of the lane's run
+  const bool leaf = valid && ((a0 - start) & (kLeaf - 1)) == 0;
+  const unsigned leaves = __ballot_sync(0xffffffffu, leaf);
+  if (leaves == 0) return;   // (never: a change starts a leaf, and 32 positions of one run hold one)
+  const int first = __ffs(leaves) - 1, final = 31 - __clz(leaves);
+  // the last leaf's positions in the next block
+  const unsigned same = __ballot_sync(0xffffffffu, k1 == __shfl_sync(0xffffffffu, k0, final));
+  const int in_block = tokens - p0 < 32 ? int(tokens - p0) : 32;
+  const int reach = in_block < 32 ? 0 : min(final, ~same == 0 ? 32 : __ffs(~same) - 1);
+  const int end = in_block + reach;   // the tokens to read: [first, end) counted from p0
+  // what becomes of the leaf that starts at this lane
+  const unsigned later = leaves & ~upto;
+  const int to = later ? __ffs(later) - 1 : end;            // one past its last position
+  const uint32_t next0 = __shfl_sync(0xffffffffu, k0, to & 31), next1 = __shfl_sync(0xffffffffu, k1, to & 31);
+  const bool goes_on = to - lane == kLeaf && (to < 32 ? next0 : next1) == k0;
+  const bool head = a0 == start;
+  const uint32_t kind = !leaf || k0 >= vocab ? kSkip : !head ? kMore : goes_on ? kFirst : kWhole;
+  const uint32_t dest = kind << 30 | (kind == kWhole ? k0 : block);
+  if (kind == kFirst && slab == 0) ws.long_runs[atomicAdd(ws.long_count, 1u)] = a0;
+
+  float2 acc[VE / 2];
+  uint32_t d = __shfl_sync(0xffffffffu, dest, first);       // of the leaf being summed
+  uint4 old = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+  for (int q = 0; q < VE / 2; ++q) acc[q] = bc2(-0.0f);
+  auto flush = [&]() {
+    const uint32_t row = d & 0x3fffffffu;
+    if (d >> 30 == kWhole) {
+      if (col) embed_store<DT, ADD>(out + int64_t(row) * nv + v, old, acc, scale);
+    } else if (d >> 30 != kSkip) {
+      float4* part = reinterpret_cast<float4*>(d >> 30 == kFirst ? ws.first_leaf : ws.more_leaves) +
+                     (uint64_t(row) * nv + v) * (VE / 4);
+      if (col) {
 #pragma unroll
-      for (int q = 0; q < VE / 2; ++q) acc[c][q] = bc2(-0.0f);
-    for (int i = 0; i < cnt; i += U) {
-      uint4 r[U][C];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const uint32_t t = __shfl_sync(0xffffffffu, my_tok, (i + j) & 31);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (i + j < cnt && v0 + 32 * c < nv) r[j][c] = __ldcs(dy + int64_t(t) * nv + v0 + 32 * c);
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (i + j < cnt) {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            float2 f[VE / 2];
-            F::unpack2(r[j][c], f);
-#pragma unroll
-            for (int q = 0; q < VE / 2; ++q) acc[c][q] = add2(acc[c][q], f[q]);
-          }
-        }
+        for (int q = 0; q < VE / 4; ++q)
+          part[q] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
       }
     }
-    if (e - s <= kLeaf) {
+  };
+  for (int i = first; i < end; i += U) {
+    uint4 r[U], o[ADD ? U : 1];
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (v0 + 32 * c < nv) embed_store<DT>(out + int64_t(id) * nv + v0 + 32 * c, acc[c], scale, add);
-    } else {
-      const uint64_t row = first ? s / kLeaf : unit;
-      float4* part = reinterpret_cast<float4*>(first ? ws.first_leaf : ws.more_leaves) + row * nv * (VE / 4);
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (v0 + 32 * c < nv) {
-#pragma unroll
-          for (int q = 0; q < VE / 4; ++q)
-            part[(v0 + 32 * c) * (VE / 4) + q] = make_float4(acc[c][2 * q].x, acc[c][2 * q].y,
-                                                             acc[c][2 * q + 1].x, acc[c][2 * q + 1].y);
-        }
+    for (int j = 0; j < U; ++j) {
+      const int x = i + j;
+      const uint32_t lo = __shfl_sync(0xffffffffu, t0, x & 31), hi = __shfl_sync(0xffffffffu, t1, x & 31);
+      if (x < end && col) r[j] = __ldcs(dy + int64_t(x < 32 ? lo : hi) * nv + v);
+      if constexpr (ADD) {
+        const uint32_t dx = __shfl_sync(0xffffffffu, dest, x & 31);
+        if (x < 32 && dx >> 30 == kWhole && col) o[j] = __ldcs(out + int64_t(dx & 0x3fffffffu) * nv + v);
       }
-      if (first && slab == 0 && lane == 0) ws.long_runs[atomicAdd(ws.counts + 1, 1u)] = run;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int x = i + j;
+      if (x < end) {   // uniform
+        if (x < 32 && ((leaves >> x) & 1u)) {
+          if (x > first) {
+            flush();
+            d = __shfl_sync(0xffffffffu, dest, x);
+#pragma unroll
+            for (int q = 0; q < VE / 2; ++q) acc[q] = bc2(-0.0f);
+          }
+          if constexpr (ADD) old = o[j];
+        }
+        float2 f[VE / 2];
+        F::unpack2(r[j], f);
+#pragma unroll
+        for (int q = 0; q < VE / 2; ++q) acc[q] = add2(acc[q], f[q]);
+      }
     }
   }
+  flush();
 }
 
 // ---------------------------------------------------------------------------
@@ -381,9 +416,9 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int add, in
 // subtrees), joined in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
-template <int DT>
+template <int DT, bool ADD>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-k_embed_join(int nv, float scale, int add, int last, EmbedWs ws, uint4* __restrict__ out) {
+k_embed_join(uint32_t tokens, int nv, float scale, int last, EmbedWs ws, uint4* __restrict__ out) {
   using F = Fmt<DT>;
   constexpr int VE = F::VE;
   griddep_trigger();
@@ -391,20 +426,20 @@ k_embed_join(int nv, float scale, int add, int last, EmbedWs ws, uint4* __restri
   __shared__ float sm[kJoinWarps][32][VE + 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const uint32_t cols = (nv + 31) / 32;
-  const uint64_t items = uint64_t(__ldcg(ws.counts + 1)) * cols;
+  const uint32_t* key = ws.key[last];
+  const uint64_t items = uint64_t(__ldcg(ws.long_count)) * cols;
   for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const uint32_t run = __ldcg(ws.long_runs + it / cols);
+    const uint32_t s = __ldcg(ws.long_runs + it / cols), id = __ldcg(key + s);
     const int v = int(it % cols) * 32 + lane;
-    const uint32_t s = __ldcg(ws.run_start + run), e = __ldcg(ws.run_start + run + 1);
+    const uint32_t e = lower_bound(key, tokens, s, tokens, id + 1);   // one past the run
     const uint32_t leaves = (e - s + kLeaf - 1) / kLeaf;
-    const uint32_t e0 = (s + kLeaf - 1) / kLeaf;
     uint32_t per = 1;                       // leaves per warp: a power of two
     while (per * kJoinWarps < leaves) per <<= 1;
     const uint32_t l0 = w * per;
     const uint32_t cnt = l0 >= leaves ? 0 : (leaves - l0 < per ? leaves - l0 : per);
     auto leaf_at = [&](uint32_t l, float2 (&f)[VE / 2]) {
       const float4* p = reinterpret_cast<const float4*>(l == 0 ? ws.first_leaf : ws.more_leaves) +
-                        (uint64_t(l == 0 ? s / kLeaf : e0 + l - 1) * nv + v) * (VE / 4);
+                        (uint64_t(s / kLeaf + l) * nv + v) * (VE / 4);
 #pragma unroll
       for (int q = 0; q < VE / 4; ++q) {
         const float4 x = __ldcg(p + q);
@@ -412,35 +447,50 @@ k_embed_join(int nv, float scale, int add, int last, EmbedWs ws, uint4* __restri
         f[2 * q + 1] = make_float2(x.z, x.w);
       }
     };
-    // a stack of pending perfect subtrees, the j-th of 2^k leaves where bit k
-    // of the leaves taken so far is set
-    float2 stack[24][VE / 2];
+    // leaves in fours (perfect subtrees, loaded at once), and a stack of pending
+    // subtrees: one of 2^k fours for every bit k of the fours taken so far
+    float2 stack[23][VE / 2], res[VE / 2];
     int top = 0;
-    if (v < nv) {
-      for (uint32_t i = 0; i < cnt; ++i) {
-        float2 cur[VE / 2];
-        leaf_at(l0 + i, cur);
-        for (uint32_t k = i; k & 1u; k >>= 1) {
-          --top;
+    if (v < nv && cnt > 0) {
+      for (uint32_t i = 0; i < cnt; i += 4) {
+        float2 f[4][VE / 2];
+        const int n = cnt - i < 4 ? int(cnt - i) : 4;
 #pragma unroll
-          for (int q = 0; q < VE / 2; ++q) cur[q] = add2(stack[top][q], cur[q]);
+        for (int j = 0; j < 4; ++j)
+          if (j < n) leaf_at(l0 + i + j, f[j]);
+        if (n > 1) {
+#pragma unroll
+          for (int q = 0; q < VE / 2; ++q) f[0][q] = add2(f[0][q], f[1][q]);
+        }
+        if (n > 3) {
+#pragma unroll
+          for (int q = 0; q < VE / 2; ++q) f[2][q] = add2(f[2][q], f[3][q]);
+        }
+        if (n > 2) {
+#pragma unroll
+          for (int q = 0; q < VE / 2; ++q) f[0][q] = add2(f[0][q], f[2][q]);
+        }
+        if (n == 4) {
+          for (uint32_t k = i / 4; k & 1u; k >>= 1) {
+            --top;
+#pragma unroll
+            for (int q = 0; q < VE / 2; ++q) f[0][q] = add2(stack[top][q], f[0][q]);
+          }
         }
 #pragma unroll
-        for (int q = 0; q < VE / 2; ++q) stack[top][q] = cur[q];
+        for (int q = 0; q < VE / 2; ++q) stack[top][q] = f[0][q];
         ++top;
       }
-      float2 res[VE / 2];
-      if (cnt > 0) {   // pending subtrees, smallest (rightmost) first
+      // pending subtrees, smallest (rightmost) first
 #pragma unroll
-        for (int q = 0; q < VE / 2; ++q) res[q] = stack[top - 1][q];
-        for (int k = top - 2; k >= 0; --k)
+      for (int q = 0; q < VE / 2; ++q) res[q] = stack[top - 1][q];
+      for (int k = top - 2; k >= 0; --k)
 #pragma unroll
-          for (int q = 0; q < VE / 2; ++q) res[q] = add2(stack[k][q], res[q]);
+        for (int q = 0; q < VE / 2; ++q) res[q] = add2(stack[k][q], res[q]);
 #pragma unroll
-        for (int q = 0; q < VE / 2; ++q) {
-          sm[w][lane][2 * q] = res[q].x;
-          sm[w][lane][2 * q + 1] = res[q].y;
-        }
+      for (int q = 0; q < VE / 2; ++q) {
+        sm[w][lane][2 * q] = res[q].x;
+        sm[w][lane][2 * q + 1] = res[q].y;
       }
     }
     __syncthreads();
@@ -460,8 +510,8 @@ k_embed_join(int nv, float scale, int add, int last, EmbedWs ws, uint4* __restri
             for (int q = 0; q < VE / 2; ++q) p[l][q] = add2(p[l][q], p[l + d][q]);
           }
       }
-      const uint32_t id = __ldcg(ws.key[last] + s);
-      embed_store<DT>(out + int64_t(id) * nv + v, p[0], scale, add);
+      uint4* at = out + int64_t(id) * nv + v;
+      embed_store<DT, ADD>(at, ADD ? *at : make_uint4(0, 0, 0, 0), p[0], scale);
     }
     __syncthreads();
   }
@@ -501,28 +551,26 @@ rn_status launch_sort(int64_t tokens, int64_t vocab, const int64_t* ids, const E
   return launch_status();
 }
 
-template <int DT>
-rn_status run_embed_bwd(int64_t tokens, int64_t vocab, int width, float scale, bool add,
-                        const int64_t* ids, const void* dy, void* dtable, const EmbedWs& ws,
+template <int DT, bool ADD>
+rn_status run_embed_bwd(int64_t tokens, int64_t vocab, int width, float scale, const int64_t* ids,
+                        const void* dy, void* dtable, const EmbedWs& ws,
                         cudaStream_t st) {
   const int nv = width / Fmt<DT>::VE;
   int last = 0;
-  rn_status e = launch_sort(tokens, vocab, ids, ws, add ? nullptr : dtable,
+  rn_status e = launch_sort(tokens, vocab, ids, ws, ADD ? nullptr : dtable,
                             size_t(vocab) * nv * 16, &last, st);
   if (e != RN_OK || tokens == 0) return e;
-  static KernelPrep prep_reduce, prep_join;
-  const uint64_t slabs = (nv + 63) / 64;
-  const uint64_t most = (uint64_t(tokens) + tokens / kLeaf + 1) * slabs;   // units, at most
-  const uint64_t want = (most + 7) / 8;
-  const int fit = prepare_kernel(k_embed_reduce<DT>, 256, 0, prep_reduce) * sm_count();
-  e = launch_pdl(k_embed_reduce<DT>, dim3(unsigned(want < uint64_t(fit) ? want : fit)), dim3(256), 0,
-                 st, uint32_t(tokens), uint32_t(vocab), nv, scale, int(add), last, ws,
-                 static_cast<const uint4*>(dy), static_cast<uint4*>(dtable));
+  static KernelPrep prep_join;
+  const uint64_t units = uint64_t((tokens + 31) / 32) * ((nv + 31) / 32);
+  e = launch_pdl(k_embed_reduce<DT, ADD>, dim3(unsigned((units + 7) / 8)), dim3(256), 0, st, uint32_t(tokens),
+                 uint32_t(vocab), nv, scale, last, ws, static_cast<const uint4*>(dy),
+                 static_cast<uint4*>(dtable));
   if (e != RN_OK || tokens <= kLeaf) return e;   // no run longer than a leaf
-  const int jfit = prepare_kernel(k_embed_join<DT>, 32 * kJoinWarps, 0, prep_join) * sm_count();
+  const int jfit = prepare_kernel(k_embed_join<DT, ADD>, 32 * kJoinWarps, 0, prep_join) * sm_count();
   const uint64_t items = uint64_t(tokens / (kLeaf + 1)) * ((nv + 31) / 32);
-  return launch_pdl(k_embed_join<DT>, dim3(unsigned(items < uint64_t(jfit) ? items : jfit)),
-                    dim3(32 * kJoinWarps), 0, st, nv, scale, int(add), last, ws,
+  const uint64_t wave = uint64_t(jfit < 2 * sm_count() ? jfit : 2 * sm_count());   // few runs are long
+  return launch_pdl(k_embed_join<DT, ADD>, dim3(unsigned(items < wave ? items : wave)),
+                    dim3(32 * kJoinWarps), 0, st, uint32_t(tokens), nv, scale, last, ws,
                     static_cast<uint4*>(dtable));
 }
 
@@ -587,12 +635,15 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
   if (tokens == 0 && accumulate) return RN_OK;
   const EmbedWs w = embed_ws(ws, tokens, width);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool add = accumulate != 0;
+#define RN_EMBED_BWD(DT_)                                                                                   \
+  return accumulate ? run_embed_bwd<DT_, true>(tokens, vocab, width, scale, ids, dy, dtable, w, st)        \
+                    : run_embed_bwd<DT_, false>(tokens, vocab, width, scale, ids, dy, dtable, w, st)
   switch (dt) {
-    case RN_BF16: return run_embed_bwd<RN_BF16>(tokens, vocab, width, scale, add, ids, dy, dtable, w, st);
-    case RN_F16: return run_embed_bwd<RN_F16>(tokens, vocab, width, scale, add, ids, dy, dtable, w, st);
-    default: return run_embed_bwd<RN_F32>(tokens, vocab, width, scale, add, ids, dy, dtable, w, st);
+    case RN_BF16: RN_EMBED_BWD(RN_BF16);
+    case RN_F16: RN_EMBED_BWD(RN_F16);
+    default: RN_EMBED_BWD(RN_F32);
   }
+#undef RN_EMBED_BWD
 }
 
 }  // extern "C"

@@ -64,9 +64,9 @@ def test_workspace_sizes(lib):
     ws = lib.embed_bwd_workspace_bytes
     assert ws(-1, H) == 0 and ws((1 << 28) + 1, H) == 0 and ws(5, 12) == 0
     assert ws(0, H) > 0
-    # 20 bytes a token and two fp32 rows for every 32 tokens, rounded up
+    # 16 bytes a token and two fp32 rows for every 32 tokens, rounded up
     n = 1 << 20
-    assert 20 * n + n // 16 * H * 4 <= ws(n, H) <= 20 * n + (n // 16 + 2) * H * 4 + n + 4096
+    assert 16 * n + n // 16 * H * 4 <= ws(n, H) <= 17 * n + (n // 16 + 2) * H * 4 + 4096
 
 
 def test_binding_refuses_before_the_library():
