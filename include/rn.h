@@ -421,7 +421,7 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
  * negative, else RN_E_ARG.
  * A row's nll and lse are bitwise the same alone or inside any batch.
  * ws: device workspace of ws_bytes >= linear_xent_fwd_workspace_bytes(rows,
- * vocab) (two floats for every 256 logits), 16-byte aligned, contents
+ * vocab) (two floats for every 128 logits), 16-byte aligned, contents
  * irrelevant.  rows == 0 enqueues nothing.
  */
 size_t linear_xent_fwd_workspace_bytes(int64_t rows, int64_t vocab);

@@ -77,7 +77,7 @@ struct EmbedWs {
   uint32_t* key[2];      // [tokens] sorted ids (vocab: no row), ping and pong
   uint32_t* tok[2];      // [tokens] their tokens
   uint32_t* long_count;  // runs longer than a leaf
-  uint32_t* long_runs;   // [tokens/32 + 1] their first positions, in any order
+  uint2* long_runs;      // [tokens/32 + 1] their positions [x, y), in any order
   // sums of the long runs' leaves: of the leaf that starts at position p, row p/32
   // (32 positions hold at most one first leaf of a long run and one later leaf)
   float* first_leaf;     // [tokens/32 + 1][H]
@@ -100,7 +100,7 @@ EmbedWs embed_ws(void* base, int64_t tokens, int width) {
     w.tok[i] = reinterpret_cast<uint32_t*>(take(n * 4));
   }
   w.long_count = reinterpret_cast<uint32_t*>(take(4));
-  w.long_runs = reinterpret_cast<uint32_t*>(take(b * 4));
+  w.long_runs = reinterpret_cast<uint2*>(take(b * 8));
   w.first_leaf = reinterpret_cast<float*>(take(b * size_t(width) * 4));
   w.more_leaves = reinterpret_cast<float*>(take(b * size_t(width) * 4));
   w.bytes = size_t(p - p0);
@@ -266,12 +266,13 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
 }
 
 // ---------------------------------------------------------------------------
-// gradient, pass 2: sums of the leaves.  A warp takes 32 sorted positions and
+// gradient, pass 2: sums of the leaves.  A warp takes 16 sorted positions and
 // 512 bytes of their columns (16 a lane), and sums the leaves that start among
 // them; the last one may reach up to 31 positions further.  The tokens' rows
 // are read eight at a time, across the ends of runs: most runs have one or two
 // tokens, and a warp to a run had too few bytes in flight (32768 tokens of 4 KB
-// rows: 95 us).  A run of one leaf is written to dE at once.
+// rows: 95 us; 55 us by 32 positions, 38 us by 16; 8 are slower again).  A run of
+// one leaf is written to dE at once.
 // ---------------------------------------------------------------------------
 // The first position of [lo, hi] whose key is at least k, one warp (key[hi] is, or
 // hi is one past the last position): 32 probes a step.
@@ -302,6 +303,7 @@ __device__ __forceinline__ void embed_store(uint4* at, const uint4& old, const f
   *at = F::pack2v(f);
 }
 
+constexpr int kSpan = 16;   // sorted positions of a unit
 template <int DT, bool ADD>
 __global__ void __launch_bounds__(256, 3)
 k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, EmbedWs ws,
@@ -317,8 +319,7 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
   const int lane = threadIdx.x & 31;
   const uint32_t slabs = (nv + 31) / 32;
   const uint64_t unit = uint64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const uint32_t block = uint32_t(unit / slabs), slab = uint32_t(unit % slabs);
-  const uint32_t p0 = block * 32;
+  const uint32_t slab = uint32_t(unit % slabs), p0 = uint32_t(unit / slabs) * kSpan;
   if (p0 >= tokens) return;
   const int v = int(slab) * 32 + lane;
   const bool col = v < nv;
@@ -336,15 +337,16 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
   const unsigned upto = 0xffffffffu >> (31 - lane);         // lanes 0..lane
   const unsigned changes = __ballot_sync(0xffffffffu, valid && k0 != (lane == 0 ? before : up));
   const uint32_t start = changes & upto ? p0 + 31 - __clz(changes & upto) : start0;   // of the lane's run
-  const bool leaf = valid && ((a0 - start) & (kLeaf - 1)) == 0;
+  const bool leaf = valid && lane < kSpan && ((a0 - start) & (kLeaf - 1)) == 0;
   const unsigned leaves = __ballot_sync(0xffffffffu, leaf);
-  if (leaves == 0) return;   // (never: a change starts a leaf, and 32 positions of one run hold one)
+  if (leaves == 0) return;   // inside a long run's leaf
   const int first = __ffs(leaves) - 1, final = 31 - __clz(leaves);
-  // the last leaf's positions in the next block
-  const unsigned same = __ballot_sync(0xffffffffu, k1 == __shfl_sync(0xffffffffu, k0, final));
-  const int in_block = tokens - p0 < 32 ? int(tokens - p0) : 32;
-  const int reach = in_block < 32 ? 0 : min(final, ~same == 0 ? 32 : __ffs(~same) - 1);
-  const int end = in_block + reach;   // the tokens to read: [first, end) counted from p0
+  // the last leaf reaches to its run's end or 32 positions, past these ones
+  const uint32_t key_f = __shfl_sync(0xffffffffu, k0, final);
+  const unsigned same0 = __ballot_sync(0xffffffffu, k0 == key_f), same1 = __ballot_sync(0xffffffffu, k1 == key_f);
+  const uint64_t same = (uint64_t(same1) << 32 | same0) >> final;
+  const int length = ~same == 0 ? kLeaf : min(__ffsll(~same) - 1, kLeaf);
+  const int end = final + length;   // the tokens to read: [first, end) counted from p0
   // what becomes of the leaf that starts at this lane
   const unsigned later = leaves & ~upto;
   const int to = later ? __ffs(later) - 1 : end;            // one past its last position
@@ -352,8 +354,15 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
   const bool goes_on = to - lane == kLeaf && (to < 32 ? next0 : next1) == k0;
   const bool head = a0 == start;
   const uint32_t kind = !leaf || k0 >= vocab ? kSkip : !head ? kMore : goes_on ? kFirst : kWhole;
-  const uint32_t dest = kind << 30 | (kind == kWhole ? k0 : block);
-  if (kind == kFirst && slab == 0) ws.long_runs[atomicAdd(ws.long_count, 1u)] = a0;
+  const uint32_t dest = kind << 30 | (kind == kWhole ? k0 : a0 / kLeaf);
+  if (slab == 0) {   // lists the long runs that start here
+    for (unsigned m = __ballot_sync(0xffffffffu, kind == kFirst); m; m &= m - 1) {
+      const int l = __ffs(m) - 1;
+      const uint32_t id = __shfl_sync(0xffffffffu, k0, l);
+      const uint32_t e = lower_bound(key, tokens, p0 + l + kLeaf, tokens, id + 1);
+      if (lane == 0) ws.long_runs[atomicAdd(ws.long_count, 1u)] = make_uint2(p0 + l, e);
+    }
+  }
 
   float2 acc[VE / 2];
   uint32_t d = __shfl_sync(0xffffffffu, dest, first);       // of the leaf being summed
@@ -383,14 +392,14 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
       if (x < end && col) r[j] = __ldcs(dy + int64_t(x < 32 ? lo : hi) * nv + v);
       if constexpr (ADD) {
         const uint32_t dx = __shfl_sync(0xffffffffu, dest, x & 31);
-        if (x < 32 && dx >> 30 == kWhole && col) o[j] = __ldcs(out + int64_t(dx & 0x3fffffffu) * nv + v);
+        if (x < kSpan && dx >> 30 == kWhole && col) o[j] = __ldcs(out + int64_t(dx & 0x3fffffffu) * nv + v);
       }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int x = i + j;
       if (x < end) {   // uniform
-        if (x < 32 && ((leaves >> x) & 1u)) {
+        if (x < kSpan && ((leaves >> x) & 1u)) {
           if (x > first) {
             flush();
             d = __shfl_sync(0xffffffffu, dest, x);
@@ -418,7 +427,7 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
 constexpr int kJoinWarps = 8;
 template <int DT, bool ADD>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-k_embed_join(uint32_t tokens, int nv, float scale, int last, EmbedWs ws, uint4* __restrict__ out) {
+k_embed_join(int nv, float scale, int last, EmbedWs ws, uint4* __restrict__ out) {
   using F = Fmt<DT>;
   constexpr int VE = F::VE;
   griddep_trigger();
@@ -429,9 +438,9 @@ k_embed_join(uint32_t tokens, int nv, float scale, int last, EmbedWs ws, uint4* 
   const uint32_t* key = ws.key[last];
   const uint64_t items = uint64_t(__ldcg(ws.long_count)) * cols;
   for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const uint32_t s = __ldcg(ws.long_runs + it / cols), id = __ldcg(key + s);
+    const uint2 run = __ldcg(ws.long_runs + it / cols);
+    const uint32_t s = run.x, e = run.y, id = __ldcg(key + s);
     const int v = int(it % cols) * 32 + lane;
-    const uint32_t e = lower_bound(key, tokens, s, tokens, id + 1);   // one past the run
     const uint32_t leaves = (e - s + kLeaf - 1) / kLeaf;
     uint32_t per = 1;                       // leaves per warp: a power of two
     while (per * kJoinWarps < leaves) per <<= 1;
@@ -561,16 +570,16 @@ rn_status run_embed_bwd(int64_t tokens, int64_t vocab, int width, float scale, c
                             size_t(vocab) * nv * 16, &last, st);
   if (e != RN_OK || tokens == 0) return e;
   static KernelPrep prep_join;
-  const uint64_t units = uint64_t((tokens + 31) / 32) * ((nv + 31) / 32);
+  const uint64_t units = uint64_t((tokens + kSpan - 1) / kSpan) * ((nv + 31) / 32);
   e = launch_pdl(k_embed_reduce<DT, ADD>, dim3(unsigned((units + 7) / 8)), dim3(256), 0, st, uint32_t(tokens),
                  uint32_t(vocab), nv, scale, last, ws, static_cast<const uint4*>(dy),
                  static_cast<uint4*>(dtable));
   if (e != RN_OK || tokens <= kLeaf) return e;   // no run longer than a leaf
   const int jfit = prepare_kernel(k_embed_join<DT, ADD>, 32 * kJoinWarps, 0, prep_join) * sm_count();
   const uint64_t items = uint64_t(tokens / (kLeaf + 1)) * ((nv + 31) / 32);
-  const uint64_t wave = uint64_t(jfit < 2 * sm_count() ? jfit : 2 * sm_count());   // few runs are long
+  const uint64_t wave = uint64_t(jfit < 4 * sm_count() ? jfit : 4 * sm_count());   // few runs are long
   return launch_pdl(k_embed_join<DT, ADD>, dim3(unsigned(items < wave ? items : wave)),
-                    dim3(32 * kJoinWarps), 0, st, uint32_t(tokens), nv, scale, last, ws,
+                    dim3(32 * kJoinWarps), 0, st, nv, scale, last, ws,
                     static_cast<uint4*>(dtable));
 }
 

@@ -53,22 +53,22 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase of that parity to complete, for about four seconds at
-// most; false (and *err set) when it did not.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t* err) {
+// most; false (and *err set) when it did not.  (Inlined: a call would spill the
+// registers that the caller holds across the wait.)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
+  if (mbar_try(bar, parity)) return true;
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  for (int i = 0; i < (1 << 24); ++i) {
-    for (int j = 0; j < 64; ++j)
-      if (mbar_try(bar, parity)) return true;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    if (t - t0 > 4000000000ull) break;
+#pragma unroll 1
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t - t0 > 4000000000ull) break;
+    }
   }
   atomicExch(err, 1u);
   return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
-  if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, err);
 }
 
 // ---- TMA ------------------------------------------------------------------------

@@ -64,9 +64,12 @@ def test_losses_and_gradients(cuda_lib, rows, width, vocab, softcap, dtype):
     _check(cuda_lib, *_case(rng, rows, width, vocab, dtype), softcap, dtype)
 
 
-def test_wide_rows(cuda_lib):
+@pytest.mark.parametrize("rows,width,vocab", [(5, 16384, 300), (9, 2056, 20001), (600, 1600, 9000)])
+def test_several_segments_of_the_width(cuda_lib, rows, width, vocab):
+    # K in segments of 512, narrow tiles (few of them) and wide ones, several
+    # tiles to a pair of CTAs
     rng = np.random.default_rng(0)
-    _check(cuda_lib, *_case(rng, 5, 16384, 300, "bf16"), 0.0, "bf16")
+    _check(cuda_lib, *_case(rng, rows, width, vocab, "bf16"), 0.0, "bf16")
 
 
 @pytest.mark.parametrize("rows", [1, 200])
@@ -121,7 +124,7 @@ def test_confident_targets_keep_their_small_loss(cuda_lib):
 
 
 def test_pieces_of_the_vocabulary_and_row_invariance(cuda_lib):
-    # 8192 rows x 40000: three chunks, each a piece of its own; 200 rows: one
+    # 8192 rows x 40000: three chunks in two pieces; 200 rows: one
     # piece.  nll, lse and dx of a row are the same bits; dw against fp64
     rng = np.random.default_rng(3)
     rows, width, vocab = 8192, 128, 40000
@@ -179,6 +182,30 @@ def test_writes_only_its_outputs(cuda_lib):
     dx, dw = cuda_lib.linear_xent_bwd(x, w, t, lse, g)
     for got, want in zip(outs, (nll, lse, dx, dw)):
         assert torch.equal(bits(got), bits(want.reshape(-1)))
+
+
+@pytest.mark.parametrize("width", [72, 256])
+def test_buffers_on_16_bytes_only(cuda_lib, width):
+    # every pointer 16 bytes past a 256-byte boundary: the same bits
+    rng = np.random.default_rng(9)
+    rows, vocab = 70, 900
+    x, w, t, g = (v.cuda() for v in _case(rng, rows, width, vocab, "bf16"))
+    nll, lse = cuda_lib.linear_xent_fwd(x, w, t)
+    dx, dw = cuda_lib.linear_xent_bwd(x, w, t, lse, g)
+
+    def shifted(n, dt):
+        return torch.empty(n + 16, dtype=dt, device="cuda")[16 // torch.empty(0, dtype=dt).element_size():][:n]
+
+    x2, w2 = shifted(rows * width, x.dtype).view(rows, width), shifted(vocab * width, x.dtype).view(vocab, width)
+    x2.copy_(x)
+    w2.copy_(w)
+    lib = cuda_lib.load()
+    ws = shifted(int(lib.linear_xent_bwd_workspace_bytes(rows, width, vocab)), torch.uint8)
+    n2, l2 = cuda_lib.linear_xent_fwd(x2, w2, t, ws=ws)
+    dx2, dw2 = cuda_lib.linear_xent_bwd(x2, w2, t, l2, g, dx=shifted(rows * width, x.dtype).view(rows, width),
+                                        dw=shifted(vocab * width, x.dtype).view(vocab, width), ws=ws)
+    for got, want in ((n2, nll), (l2, lse), (dx2, dx), (dw2, dw)):
+        assert torch.equal(bits(got), bits(want))
 
 
 def test_captured_and_replayed_with_other_targets(cuda_lib):

@@ -71,8 +71,8 @@ def test_backward_checks(lib, kw, want):
 def test_workspace_sizes(lib):
     f, b = lib.linear_xent_fwd_workspace_bytes, lib.linear_xent_bwd_workspace_bytes
     assert f(0, V) == 0 and f(5, 0) == 0 and b(0, H, V) == 0 and b(5, 12, V) == 0
-    # two floats for every 256 logits (rows rounded up to 256), and a float a row
-    assert f(512, 2560) == 512 * 10 * 8 + 512 * 4
+    # two floats for every 128 logits (rows rounded up to 256), and a float a row
+    assert 512 * 20 * 8 + 512 * 4 <= f(512, 2560) <= 512 * 20 * 8 + 512 * 4 + 256
     # never the logits of the whole vocabulary of a large batch
     assert b(65536, 2048, 151936) < 65536 * 151936 * 2 // 4
 
