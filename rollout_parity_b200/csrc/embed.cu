@@ -9,10 +9,11 @@
 // start, a leaf is summed in token order, and a run's leaves are joined by the
 // level-by-level pairwise tree.  So a row of dE depends on its own tokens only,
 // bitwise, wherever they stand in the batch and whatever the other tokens are.
-// Three kernels: k_embed_sort (which also clears dE with the CTAs that do not
-// sort), k_embed_reduce, k_embed_join.
+// Three kernels: k_embed_sort, k_embed_reduce, k_embed_join; the first two also
+// clear the rows of dE that no token has.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "rn_checks.cuh"
@@ -109,7 +110,7 @@ EmbedWs embed_ws(void* base, int64_t tokens, int width) {
 
 // ---------------------------------------------------------------------------
 // gradient, pass 1: cluster 0 sorts the tokens by id (stable least-significant-
-// digit radix sort); the other clusters clear dE meanwhile.
+// digit radix sort); the other clusters clear rows of dE meanwhile.
 // A warp owns a contiguous piece of the positions.  Per pass: a histogram of
 // each warp's piece, prefix sums over the warps, the cluster's CTAs
 // (distributed shared memory) and the bins, then the scatter in order.
@@ -269,10 +270,12 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
 // gradient, pass 2: sums of the leaves.  A warp takes 16 sorted positions and
 // 512 bytes of their columns (16 a lane), and sums the leaves that start among
 // them; the last one may reach up to 31 positions further.  The tokens' rows
-// are read eight at a time, across the ends of runs: most runs have one or two
-// tokens, and a warp to a run had too few bytes in flight (32768 tokens of 4 KB
-// rows: 95 us; 55 us by 32 positions, 38 us by 16; 8 are slower again).  A run of
-// one leaf is written to dE at once.
+// are read four at a time, across the ends of runs: most runs have one or two
+// tokens, and a warp to a run had too few bytes in flight.  A run of one leaf is
+// written to dE at once.  Measured, 32768 tokens of 4 KB rows over 151936, the
+// whole gradient: a warp to a run and 1 KB 227 us, 32 positions 187, 16 170 (8: 177);
+// with the clearing here too 180, then eight tokens in flight at 24 warps an SM
+// against four at 32 warps 163.
 // ---------------------------------------------------------------------------
 // The first position of [lo, hi] whose key is at least k, one warp (key[hi] is, or
 // hi is one past the last position): 32 probes a step.
@@ -303,13 +306,32 @@ __device__ __forceinline__ void embed_store(uint4* at, const uint4& old, const f
   *at = F::pack2v(f);
 }
 
+// Clears the rows of [v0, v1), at most 32, that no token has; one warp.
+__device__ __forceinline__ void clear_rows(const uint32_t* key, uint32_t tokens, uint32_t v0, uint32_t v1,
+                                           int nv, uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  unsigned hit = 0;
+  uint32_t p = lower_bound(key, tokens, 0, tokens, v0);
+  while (true) {   // uniform; every turn finds a row of its own or is the last
+    const uint32_t k = p + lane < tokens ? __ldcg(key + p + lane) : 0xffffffffu;
+    const bool in = k < v1;
+    hit |= __reduce_or_sync(0xffffffffu, in ? 1u << (k - v0) : 0u);
+    if (!__all_sync(0xffffffffu, in)) break;
+    p = lower_bound(key, tokens, p + 32, tokens, __shfl_sync(0xffffffffu, k, 31) + 1);   // past that row's run
+  }
+  for (uint32_t r = v0; r < v1; ++r) {
+    if ((hit >> (r - v0)) & 1u) continue;
+    for (int v = lane; v < nv; v += 32) out[int64_t(r) * nv + v] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 constexpr int kSpan = 16;   // sorted positions of a unit
 template <int DT, bool ADD>
-__global__ void __launch_bounds__(256, 3)
-k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, EmbedWs ws,
-               const uint4* __restrict__ dy, uint4* __restrict__ out) {
+__global__ void __launch_bounds__(256, ADD ? 3 : 4)
+k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, EmbedWs ws, uint32_t cleared,
+               uint32_t clear_step, uint32_t sum_blocks, const uint4* __restrict__ dy, uint4* __restrict__ out) {
   using F = Fmt<DT>;
-  constexpr int VE = F::VE, U = ADD ? 4 : 8;   // tokens (and with ADD, old rows) in flight
+  constexpr int VE = F::VE, U = 4;   // tokens (and with ADD, old rows) in flight
   constexpr uint32_t kNone = 0xffffffffu;
   enum { kSkip = 0, kWhole = 1, kFirst = 2, kMore = 3 };   // where a leaf's sum goes
   griddep_trigger();
@@ -318,7 +340,16 @@ k_embed_reduce(uint32_t tokens, uint32_t vocab, int nv, float scale, int last, E
   const uint32_t* tok = ws.tok[last];
   const int lane = threadIdx.x & 31;
   const uint32_t slabs = (nv + 31) / 32;
-  const uint64_t unit = uint64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  // the blocks that sum and those that clear, spread evenly among one another
+  const uint64_t sums_before = uint64_t(blockIdx.x) * sum_blocks / gridDim.x;
+  if constexpr (!ADD) {
+    if (uint64_t(blockIdx.x + 1) * sum_blocks / gridDim.x == sums_before) {
+      const uint64_t v0 = cleared + ((uint64_t(blockIdx.x) - sums_before) * 8 + (threadIdx.x >> 5)) * clear_step;
+      if (v0 < vocab) clear_rows(key, tokens, uint32_t(v0), uint32_t(min(v0 + clear_step, uint64_t(vocab))), nv, out);
+      return;
+    }
+  }
+  const uint64_t unit = sums_before * (blockDim.x / 32) + (threadIdx.x >> 5);
   const uint32_t slab = uint32_t(unit % slabs), p0 = uint32_t(unit / slabs) * kSpan;
   if (p0 >= tokens) return;
   const int v = int(slab) * 32 + lane;
@@ -566,14 +597,22 @@ rn_status run_embed_bwd(int64_t tokens, int64_t vocab, int width, float scale, c
                         cudaStream_t st) {
   const int nv = width / Fmt<DT>::VE;
   int last = 0;
+  // Rows cleared beside the sort, which takes about 8 us and 1 us for every 4096
+  // tokens, at 5 MB a us; the others are cleared beside the sums, where the rows
+  // that a token has need no clearing.
+  const int64_t beside = (int64_t(8) + tokens / 4096) * 5000000 / (int64_t(nv) * 16);
+  const int64_t cleared = ADD ? vocab : tokens == 0 || beside > vocab ? vocab : beside;
   rn_status e = launch_sort(tokens, vocab, ids, ws, ADD ? nullptr : dtable,
-                            size_t(vocab) * nv * 16, &last, st);
+                            size_t(cleared) * nv * 16, &last, st);
   if (e != RN_OK || tokens == 0) return e;
   static KernelPrep prep_join;
   const uint64_t units = uint64_t((tokens + kSpan - 1) / kSpan) * ((nv + 31) / 32);
-  e = launch_pdl(k_embed_reduce<DT, ADD>, dim3(unsigned((units + 7) / 8)), dim3(256), 0, st, uint32_t(tokens),
-                 uint32_t(vocab), nv, scale, last, ws, static_cast<const uint4*>(dy),
-                 static_cast<uint4*>(dtable));
+  // a clearing warp takes about 32 KB, 32 rows at most
+  const int64_t step = std::min<int64_t>(32, std::max<int64_t>(1, 32768 / (int64_t(nv) * 16)));
+  const uint64_t sums = (units + 7) / 8, clears = (vocab - cleared + 8 * step - 1) / (8 * step);
+  e = launch_pdl(k_embed_reduce<DT, ADD>, dim3(unsigned(sums + clears)), dim3(256), 0, st, uint32_t(tokens),
+                 uint32_t(vocab), nv, scale, last, ws, uint32_t(cleared), uint32_t(step), uint32_t(sums),
+                 static_cast<const uint4*>(dy), static_cast<uint4*>(dtable));
   if (e != RN_OK || tokens <= kLeaf) return e;   // no run longer than a leaf
   const int jfit = prepare_kernel(k_embed_join<DT, ADD>, 32 * kJoinWarps, 0, prep_join) * sm_count();
   const uint64_t items = uint64_t(tokens / (kLeaf + 1)) * ((nv + 31) / 32);

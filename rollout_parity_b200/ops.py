@@ -456,13 +456,14 @@ def layernorm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor] = 
     if b is not None:
         _vec("b", b, width, x.device)
     y = torch.empty_like(x) if y is None else _mat("y", y, x)
-    if want_stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if mean is None else mean
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd is None else rstd
     if mean is not None:
         _vec("mean", mean, rows, x.device)
+    elif want_stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
     if rstd is not None:
         _vec("rstd", rstd, rows, x.device)
+    elif want_stats:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
     _launch("layernorm_fwd", x, stream, rows, width, eps, dt, _ptr(x), _ptr(w), _ptr(b), _ptr(y),
             _ptr(mean), _ptr(rstd))
     return y, mean, rstd
