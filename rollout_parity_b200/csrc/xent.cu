@@ -95,6 +95,11 @@ __device__ __forceinline__ float exp2_approx(float x) {   // 2 units in the last
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // r = 1 / (1 + e^(2u)): tanh(u) = 1 - 2r and 1 - tanh(u)^2 = 4r(1 - r); the
 // absolute error of both is a few 2^-24
 __device__ __forceinline__ float half_tail(float u) {
@@ -375,22 +380,34 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (act && cols > 0) {
           float mc[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-          for (int i = 4; i < kStatCols; ++i) mc[i & 3] = fmaxf(mc[i & 3], z[i]);
+          for (int i = 4; i + 8 <= kStatCols; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mc[k] = max3(mc[k], z[i + k], z[i + 4 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mc[k] = fmaxf(mc[k], z[kStatCols - 4 + k]);
           const float m = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+          // exp(z - m) as 2^(z log2e - t) with t = m log2e rounded: one multiply-add
+          // an element; what t was rounded by, r, is common to all and taken out of
+          // the sum (so the largest element counts as exactly 1)
+          const float t = m * kLog2e, r = fmaf(m, kLog2e, -t);
           float2 s2[4] = {bc2(0.0f), bc2(0.0f), bc2(0.0f), bc2(0.0f)};
 #pragma unroll
           for (int i = 0; i < kStatCols; i += 2) {
-            const float2 e = mul2(add2(make_float2(z[i], z[i + 1]), bc2(-m)), bc2(kLog2e));
-            s2[(i >> 1) & 3] = add2(s2[(i >> 1) & 3], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
+            const float2 e = fma2(make_float2(z[i], z[i + 1]), bc2(kLog2e), bc2(-t));
+            s2[(i >> 1) & 3] = __fadd2_rn(s2[(i >> 1) & 3], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
           }
-          const float2 u = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
-          a.part[int64_t(col0 / kStatCols) * a.rows_pad + row] = make_float2(m, u.x + u.y);
+          const float2 u2 = __fadd2_rn(__fadd2_rn(s2[0], s2[1]), __fadd2_rn(s2[2], s2[3]));
+          const float u = (u2.x + u2.y) * exp2_approx(-r);
+          a.part[int64_t(col0 / kStatCols) * a.rows_pad + row] = make_float2(m, u);
         }
       } else if constexpr (MODE == kDz) {
         const bool act = row < kept;
         const int tg = act ? __ldcg(a.tgt_k + row) - a.v0 - col0 : -1;
-        const float lse = act ? __ldcg(a.lse_k + row) : 0.0f;
+        // exp(z - lse) as 2^(z log2e - lse2), and what lse2 was rounded by in the
+        // factor (a likely target's p - 1 would lose digits to it)
+        const float lse = act ? __ldcg(a.lse_k + row) : 0.0f, lse2 = lse * kLog2e;
         const float g = act ? __ldcg(a.g_k + row) : 0.0f;
+        const float gp = g * exp2_approx(-fmaf(lse, kLog2e, -lse2));
         const int cols = a.vocab - a.v0 - col0;
         uint16_t* dst = static_cast<uint16_t*>(a.dz) + int64_t(row) * a.ld + col0;
         if (!wait_acc()) break;
@@ -398,25 +415,41 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
           tmem_ld_wait();
-          float d[32];
+          float2 d[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float z = __uint_as_float(r[i]), slope = g;
+          for (int i = 0; i < 16; ++i) {
+            float2 z = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), slope = bc2(gp);
             if (CAP) {
-              const float h = half_tail(z * a.inv_cap);
-              z = a.cap * fmaf(-2.0f, h, 1.0f);
-              slope *= 4.0f * h * (1.0f - h);
+              const float2 h = make_float2(half_tail(z.x * a.inv_cap), half_tail(z.y * a.inv_cap));
+              z = mul2(bc2(a.cap), fma2(bc2(-2.0f), h, bc2(1.0f)));
+              const float2 f = mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f)));
+              slope = mul2(slope, f);
+              r[2 * i] = __float_as_uint(f.x);           // (for the target, below)
+              r[2 * i + 1] = __float_as_uint(f.y);
             }
-            const float prob = exp2_approx((z - lse) * kLog2e);
-            d[i] = slope * (tg == c + i ? prob - 1.0f : prob);
-            if (!act || c + i >= cols) d[i] = 0.0f;   // no row, or no column: exactly nothing
+            const float2 e = fma2(z, bc2(kLog2e), bc2(-lse2));
+            d[i] = mul2(slope, make_float2(exp2_approx(e.x), exp2_approx(e.y)));
+          }
+          if (unsigned(tg - c) < 32u) {   // the target's 1
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (tg == c + 2 * i) d[i].x -= CAP ? g * __uint_as_float(r[2 * i]) : g;
+              if (tg == c + 2 * i + 1) d[i].y -= CAP ? g * __uint_as_float(r[2 * i + 1]) : g;
+            }
+          }
+          if (!act || cols < c + 32) {    // no row, or no column: exactly nothing
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (!act || c + 2 * i >= cols) d[i].x = 0.0f;
+              if (!act || c + 2 * i + 1 >= cols) d[i].y = 0.0f;
+            }
           }
 #pragma unroll
-          for (int v = 0; v < 32; v += 16) {
+          for (int v = 0; v < 2; ++v) {
             uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = F::pack2(d[v + 2 * i], d[v + 2 * i + 1]);
-            st_32(dst + c + v, o);
+            for (int i = 0; i < 8; ++i) o[i] = F::pack2(d[8 * v + i].x, d[8 * v + i].y);
+            st_32(dst + c + 16 * v, o);
           }
         }
         free_acc();
