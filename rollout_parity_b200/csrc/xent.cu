@@ -21,6 +21,7 @@
 // the kept rows in order, in the tensor cores' fp32 accumulator.
 #include <cuda.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -118,7 +119,8 @@ struct TileAt {
 // row tiles of one column tile after each other.  kGrad: the dx tiles, whose K is
 // a chunk of the vocabulary, are dealt out first; the dW tiles, whose K is the
 // kept rows, fill up the pairs that got one dx tile less, so that all pairs have
-// about the same number of K blocks (one more a tile for its epilogue).
+// about the same number of K blocks (one more a tile for its epilogue, which takes
+// as long as five).
 template <int MODE>
 struct TileWalk {
   int mt, nt, pair, pairs, tiles;
@@ -135,7 +137,7 @@ struct TileWalk {
       const int dw_tiles = a.dw ? (cols + kTileM - 1) / kTileM * nt : 0;
       const int more = dx_tiles % pairs;   // pairs with one dx tile more
       my_dx = dx_tiles / pairs + (pair < more);
-      const float lead = float(min(a.chunk, cols) / kTileK + 1) / float((kept + kTileK - 1) / kTileK + 1);
+      const float lead = float(min(a.chunk, cols) / kTileK + 1) / float(max((kept + kTileK - 1) / kTileK, 5) + 1);
       // dW tiles of a pair with one dx tile more: that dx tile's worth (`lead`) below the others
       const float even = (float(dw_tiles) - float(pairs - more) * lead) / float(pairs);
       const int few = more > 0 && even > 0.0f ? int(even) : 0;
@@ -805,19 +807,25 @@ FwdWs xent_fwd_ws(void* base, int64_t rows, int64_t vocab) {
   return w;
 }
 
-// The vocabulary in chunks of at most 16384 columns (dx is summed over them, so
-// the size depends on V only); a piece is as many chunks as keep dz within
-// 512 MB, at least one (4096 rows: 64 MB pieces 7.05 ms, 256 MB 6.50, 512 MB 6.41).
-constexpr int64_t kMostChunk = 16384;
+// The vocabulary in chunks that dx is summed over: at most 16384 columns, and
+// down to 8192 while the chunks of one row tile make fewer than 64 tiles of dx, so
+// that few rows have tiles for every pair of CTAs (100 x 1024 x 50000 step 142 us in
+// chunks of 16384, 122 in 8192, 132 in 4096, 4096 rows of it 1419, 1401, 1498: a
+// smaller chunk costs many rows the writing and reading of its product).  The
+// number depends on V and H only, so a row's dx does not depend on the rows.
+// A piece is as many chunks as keep dz within 512 MB, at least one (4096 x 2048 x
+// 151936 step: 64 MB pieces 7.05 ms, 256 MB 6.50, 512 MB 6.41).
+constexpr int64_t kMostChunk = 16384, kLeastChunk = 8192, kFewTiles = 64;
 constexpr int64_t kDzBudget = int64_t(512) << 20;
 struct BwdPlan {
   int64_t rows_pad;
   int chunk, chunks, per_piece, pieces;
 };
-BwdPlan xent_plan(int64_t rows, int64_t vocab) {
+BwdPlan xent_plan(int64_t rows, int width, int64_t vocab) {
   BwdPlan p;
   p.rows_pad = up(rows, kTileM);
-  p.chunk = int(up(ceil_div(vocab, ceil_div(vocab, kMostChunk)), 256));
+  const int64_t spread = std::min(ceil_div(vocab, kLeastChunk), ceil_div(kFewTiles, ceil_div(width, kTileN)));
+  p.chunk = int(up(ceil_div(vocab, std::max(ceil_div(vocab, kMostChunk), spread)), 256));
   p.chunks = int(ceil_div(vocab, p.chunk));
   const int64_t fit = kDzBudget / (p.rows_pad * p.chunk * 2);
   const int64_t g = fit < 1 ? 1 : (fit < p.chunks ? fit : p.chunks);
@@ -891,7 +899,7 @@ template <int DT>
 rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, const void* w,
                        const int64_t* target, const float* lse, const float* dnll, float cap, void* dx, void* dw,
                        void* ws, cudaStream_t st) {
-  const BwdPlan p = xent_plan(rows, vocab);
+  const BwdPlan p = xent_plan(rows, width, vocab);
   const BwdWs b = xent_bwd_ws(ws, rows, width, p);
   rn_status e = launch_pdl(k_xent_scan, dim3(1), dim3(1024), 0, st, int(rows), int(vocab), int(DT == RN_F16),
                            target, dnll, b.head, b.pos, b.kept_row);
@@ -993,7 +1001,7 @@ rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype d
 
 size_t linear_xent_bwd_workspace_bytes(int64_t rows, int32_t width, int64_t vocab) {
   if (!xent_sizes_ok(rows, vocab) || rows == 0 || !width_ok(width)) return 0;
-  return xent_bwd_ws(nullptr, rows, width, xent_plan(rows, vocab)).bytes;
+  return xent_bwd_ws(nullptr, rows, width, xent_plan(rows, width, vocab)).bytes;
 }
 
 rn_status linear_xent_bwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype dt, const void* x,
