@@ -46,7 +46,8 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kHalf = 16384;                             // a CTA's half of A or B, a stage
 constexpr int kStages = 6, kStageBytes = 2 * kHalf;      // 192 KB
 constexpr int kThreads = 384;                            // loader, MMA, two idle, eight epilogue warps
-constexpr int kTileSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kOutBytes = 4096;                          // a warp's part of the result: 32 rows of 128 bytes
+constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
 constexpr int kStatCols = 128;                           // columns of one (max, sum) of the forward
 // The forward sums K in segments of 1024: the tensor cores cut each addition to
 // the accumulator off instead of rounding it, an error that grows with the
@@ -78,11 +79,12 @@ struct XentArgs {
   const int* tgt_k;        // backward, by kept row: target,
   const float* lse_k;      //   lse
   const float* g_k;        //   dnll * scale
+  void* dz;                // kDz: [rows_pad][ld]
   float2* part;            // kFwd: [ceil(vocab/128)][rows_pad] (max, sum)
   float* zt;               // kFwd: [rows_pad] the target's s
-  void* dz;                // kDz: [rows_pad][ld]
   float* slab;             // kGrad: [chunks][rows_pad][H], NULL: no dx
   void* dw;                // kGrad: [vocab][H], NULL: no dW
+  int dw_32;               // the rows of dW start on 32 bytes
 };
 
 // Set when a wait in k_xent_tile ran out: from then on the operator's results
@@ -181,13 +183,10 @@ struct TileWalk {
   }
 };
 
-__device__ __forceinline__ void st_32(void* p, const uint32_t (&r)[8]) {   // 32 bytes, aligned
+__device__ __forceinline__ void st_32(void* p, const uint32_t* r) {   // 32 bytes, aligned
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-}
-__device__ __forceinline__ void st_16(void* p, const uint32_t* r) {
-  *static_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Warp 0 loads the operands' tiles by TMA into a ring of stages, warp 1 of the
@@ -195,17 +194,18 @@ __device__ __forceinline__ void st_16(void* p, const uint32_t* r) {
 // (two of 256 columns in tensor memory, so that the next products run
 // meanwhile) and finish the tile, four warps the left half of the columns and
 // four the right.
-// Operands: kFwd, kDz  a: x, b: W;  kGrad  a: dz (boxes of 128 rows), b: W (boxes
-// of 64), c: dz again (boxes of 64), d: x (boxes of 64).
+// Tensor maps: kFwd, kDz  a: x, b: W;  kGrad  a: dz (boxes of 128 rows), b: W (boxes
+// of 64), c: dz again (boxes of 64), d: x (boxes of 64), e: dW, where it is written
+// by TMA.
 template <int DT, int MODE, bool CAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d,
-            const XentArgs a) {
+            const __grid_constant__ CUtensorMap map_e, const XentArgs a) {
   using F = Fmt<DT>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t bars = base + kStages * kStageBytes + 8 * kOutBytes;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
@@ -327,6 +327,25 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const int c0 = ((warp - 4) >> 2) * 128;
     const uint32_t lanes = tmem + (uint32_t(q * 32) << 16) + c0;
     const int my_row = int(rank) * 128 + q * 32 + lane;
+    const uint32_t out = base + kStages * kStageBytes + (warp - 4) * kOutBytes;
+    // A dz, dx or dW tile: a thread holds a row of it and stores 32 bytes at a time.
+    // Where dW's rows start on 16 bytes only, it leaves through shared memory by
+    // TMA instead (16-byte stores against it: 509 x 1032 x 32771 step 205 and 188 us;
+    // for rows on 32 bytes TMA was up to 4% slower).
+    // A row of the warp's 32 x 32 words, its 16-byte pieces swizzled as the tensor
+    // map says, into the warp's buffer; then one lane stores the box at (c0, c1).
+    auto store_box = [&](const CUtensorMap* map, const uint32_t (&w)[32], int c0, int c1, bool inside) {
+      if (lane == 0) tma_store_wait_read();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                     "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0 && inside) tma_store(map, out, c0, c1);
+    };
     int n = 0;   // accumulators
     bool ok = true;
     for (int j = 0; j < count && ok; ++j) {
@@ -413,6 +432,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const int cols = a.vocab - a.v0 - col0;
         uint16_t* dst = static_cast<uint16_t*>(a.dz) + int64_t(row) * a.ld + col0;
         if (!wait_acc()) break;
+#pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
@@ -447,58 +467,54 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
           }
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = F::pack2(d[8 * v + i].x, d[8 * v + i].y);
-            st_32(dst + c + 16 * v, o);
-          }
+          for (int i = 0; i < 16; ++i) r[i] = F::pack2(d[i].x, d[i].y);
+          if (c == 96) free_acc();
+          st_32(dst + c, r);
+          st_32(dst + c + 16, r + 8);
         }
-        free_acc();
       } else if (p.chunk >= 0) {   // dx
         float* dst = a.slab + (int64_t(p.chunk) * a.rows_pad + row) * a.H + col0;
         if (!wait_acc()) break;
-        for (int c = 0; c < 128 && col0 + c < a.H; c += 32) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
           tmem_ld_wait();
+          if (c == 96) free_acc();
           if (row < kept) {
 #pragma unroll
             for (int v = 0; v < 32; v += 8)
-              if (col0 + c + v < a.H) st_32(dst + c + v, *reinterpret_cast<uint32_t(*)[8]>(&r[v]));
+              if (col0 + c + v < a.H) st_32(dst + c + v, r + v);
           }
         }
-        free_acc();
       } else {                     // dW
-        const int64_t v_row = int64_t(a.v0) + row;
-        const bool act = row < a.ld && v_row < a.vocab;
         const float inv = __ldcg(a.head + 2);
-        uint16_t* dst = static_cast<uint16_t*>(a.dw) + v_row * a.H + col0;
-        const bool wide = a.H % 16 == 0 && (uintptr_t(a.dw) & 31) == 0;   // rows start on 32 bytes
+        const int v_row = a.v0 + p.m0 + int(rank) * 128 + q * 32;   // the warp's first row
+        uint16_t* dst = static_cast<uint16_t*>(a.dw) + int64_t(v_row + lane) * a.H + col0;
         if (!wait_acc()) break;
-        for (int c = 0; c < 128 && col0 + c < a.H; c += 32) {
+        uint32_t w[32];            // 64 columns
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
           tmem_ld_wait();
-          uint32_t o[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)   // no kept row: the accumulator was never written
-            o[i] = p.kblocks == 0 ? 0u : F::pack2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
-          if (act) {
-            if (wide) {
+            w[c % 64 / 2 + i] = p.kblocks == 0 ? 0u : F::pack2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+          if (c == 96) free_acc();
+          if (c % 64 == 32 && col0 + c - 32 < a.H) {   // uniform
+            if (a.dw_32) {
 #pragma unroll
-              for (int v = 0; v < 2; ++v)
-                if (col0 + c + 16 * v < a.H) st_32(dst + c + 16 * v, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * v]));
+              for (int v = 0; v < 64; v += 16)
+                if (v_row + lane < a.vocab && col0 + c - 32 + v < a.H) st_32(dst + c - 32 + v, w + v / 2);
             } else {
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                if (col0 + c + 8 * v < a.H) st_16(dst + c + 8 * v, &o[4 * v]);
+              store_box(&map_e, w, col0 + c - 32, v_row, v_row < a.vocab);
             }
           }
         }
-        free_acc();
       }
     }
+    if (lane == 0) tma_store_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -746,25 +762,26 @@ EncodeTiled encode_tiled() {
   return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A row-major matrix of 16-bit elements read in boxes of 64 columns (128 bytes,
-// swizzled) by `box_rows` rows; what lies outside reads as zero.
+// A row-major matrix read or written in boxes of 128 bytes (swizzled) by `box_rows`
+// rows; what lies outside reads as zero.
 rn_status make_map(CUtensorMap* map, rn_dtype dt, const void* p, int64_t rows, int64_t cols, int64_t ld,
                    int box_rows) {
   const EncodeTiled enc = encode_tiled();
   if (!enc) return cuda_failed(int(cudaErrorNotSupported));
   const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-  const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
-  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, steps[2] = {1, 1};
+  const cuuint64_t strides[1] = {cuuint64_t(ld) * elem_bytes(dt)};
+  const cuuint32_t box[2] = {cuuint32_t(128 / elem_bytes(dt)), cuuint32_t(box_rows)}, steps[2] = {1, 1};
   const CUresult e =
-      enc(map, dt == RN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+      enc(map, dt == RN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+               : dt == RN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
           const_cast<void*>(p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return e == CUDA_SUCCESS ? RN_OK : cuda_failed(int(cudaErrorInvalidValue));
 }
 
-// The tensor maps of a launch; kFwd and kDz use a and b only.
+// The tensor maps of a launch (see k_xent_tile); those it does not use are zeros.
 struct TileMaps {
-  CUtensorMap a, b, c, d;
+  CUtensorMap a, b, c, d, e;
 };
 template <int DT, int MODE, bool CAP>
 rn_status launch_tile(const TileMaps& m, const XentArgs& a, int64_t most_tiles, cudaStream_t st) {
@@ -773,7 +790,7 @@ rn_status launch_tile(const TileMaps& m, const XentArgs& a, int64_t most_tiles, 
   const int64_t pairs = sm_count() / 2;
   const int64_t want = most_tiles < pairs ? most_tiles : pairs;
   return launch_pdl(k_xent_tile<DT, MODE, CAP>, dim3(unsigned(2 * (want < 1 ? 1 : want))), dim3(kThreads),
-                    kTileSmem, st, m.a, m.b, m.c, m.d, a);
+                    kTileSmem, st, m.a, m.b, m.c, m.d, m.e, a);
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -936,6 +953,8 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
   if (e == RN_OK) e = make_map(&grad.b, rn_dtype(DT), w, vocab, width, width, 64);
   if (e == RN_OK) e = make_map(&grad.c, rn_dtype(DT), b.dz, p.rows_pad, ld, ld, 64);
   if (e == RN_OK) e = make_map(&grad.d, rn_dtype(DT), b.xk, p.rows_pad, width, width, 64);
+  a.dw_32 = width % 16 == 0 && (uintptr_t(dw) & 31) == 0;
+  if (e == RN_OK && dw && !a.dw_32) e = make_map(&grad.e, rn_dtype(DT), dw, vocab, width, width, 32);
   if (e != RN_OK) return e;
   const int64_t mt = p.rows_pad / kTileM, ht = ceil_div(width, kTileN);
   for (int piece = 0; piece < p.pieces; ++piece) {
