@@ -543,18 +543,19 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restri
   const int row = blockIdx.x * 32 + lane;
   float2 s = make_float2(-INFINITY, 0.0f);
   if (row < rows) {
-    for (int t0 = j; t0 < tiles; t0 += 32 * 8) {   // eight loads in flight, one rescaling
-      float2 v[8];
+    constexpr int kAhead = 16;   // loads in flight, to one rescaling
+    for (int t0 = j; t0 < tiles; t0 += 32 * kAhead) {
+      float2 v[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kAhead; ++i)
         v[i] = t0 + 32 * i < tiles ? __ldcg(part + int64_t(t0 + 32 * i) * rows_pad + row) : make_float2(-INFINITY, 0.0f);
       float m = s.x;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i].x);
+      for (int i = 0; i < kAhead; ++i) m = fmaxf(m, v[i].x);
       const float base = m == -INFINITY ? 0.0f : m;   // (then every exponential is of -inf)
       float sum = s.y * exp2_approx((s.x - base) * kLog2e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[i].y, exp2_approx((v[i].x - base) * kLog2e), sum);
+      for (int i = 0; i < kAhead; ++i) sum = fmaf(v[i].y, exp2_approx((v[i].x - base) * kLog2e), sum);
       s = make_float2(m, sum);
     }
   }
@@ -580,104 +581,77 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restri
 }
 
 // ---------------------------------------------------------------------------
-// backward: the rows that carry a loss, listed in order by one CTA, and the
-// power of two that dz is scaled by (fp16 only: dz is at most max |dnll|, and
-// 2^15 / that keeps small probabilities out of fp16's subnormals; bf16 has
-// fp32's exponents and takes 1)
+// backward: the rows that carry a loss, next to each other and in order, with
+// their targets, lse and scaled gradients, and the power of two that dz is scaled
+// by (fp16 only: dz is at most max |dnll|, and 2^15 / that keeps small
+// probabilities out of fp16's subnormals; bf16 has fp32's exponents and takes
+// 1).  Every CTA looks at all targets (12 bytes a row, from L2) to know how many
+// kept rows come before its own: one launch in place of a scan and a gather, 4 us
+// less for few rows.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(1024)
-k_xent_scan(int rows, int vocab, int fp16, const int64_t* __restrict__ target,
-            const float* __restrict__ dnll, float* __restrict__ head, int* __restrict__ pos,
-            int* __restrict__ kept_row) {
+__global__ void __launch_bounds__(256)
+k_xent_pack(int rows, int rows_per_cta, int vocab, int nv, int fp16, const uint4* __restrict__ x,
+            const int64_t* __restrict__ target, const float* __restrict__ lse, const float* __restrict__ dnll,
+            float* __restrict__ head, int* __restrict__ pos, uint4* __restrict__ xk, int* __restrict__ tgt_k,
+            float* __restrict__ lse_k, float* __restrict__ g_k) {
   griddep_trigger();
   griddep_wait();
-  constexpr int kAhead = 8;   // groups of 1024 rows at a time
-  __shared__ int count[kAhead * 32];
-  __shared__ float warp_max[32];
-  __shared__ int total;
+  __shared__ int s_before[8], s_all[8], s_row[256];
+  __shared__ float s_top[8];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  int done = 0;
+  const int start = min(int64_t(blockIdx.x) * rows_per_cta, int64_t(rows));
+  const int end = min(int64_t(start) + rows_per_cta, int64_t(rows));
+  int before = 0, all = 0;
   float top = 0.0f;
-  for (int r0 = 0; r0 < rows; r0 += 1024 * kAhead) {
-    int64_t t[kAhead];
-    float g[kAhead];
+  for (int64_t r0 = tid; r0 < rows; r0 += 256 * 8) {
+    int64_t t[8];
+    float g[8];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = r0 + 1024 * i + tid;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + 256 * i;
       t[i] = r < rows ? __ldg(target + r) : -1;
       g[i] = r < rows ? __ldg(dnll + r) : 0.0f;
     }
-    unsigned kept[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const bool keep = t[i] >= 0 && t[i] < vocab;
-      if (keep) top = fmaxf(top, fabsf(g[i]));
-      kept[i] = __ballot_sync(0xffffffffu, keep);
-      if (lane == 0) count[i * 32 + w] = __popc(kept[i]);
-    }
-    __syncthreads();
-    if (w == 0) {   // exclusive prefix over the groups' warps, in row order
-      int before = done;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int c = count[i * 32 + lane];
-        int x = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += u;
-        }
-        count[i * 32 + lane] = before + x - c;
-        before += __shfl_sync(0xffffffffu, x, 31);
+    for (int i = 0; i < 8; ++i) {
+      if (t[i] >= 0 && t[i] < vocab) {
+        ++all;
+        before += r0 + 256 * i < start;
+        top = fmaxf(top, fabsf(g[i]));
       }
-      if (lane == 0) total = before;
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = r0 + 1024 * i + tid;
-      const bool keep = (kept[i] >> lane) & 1u;
-      const int at = count[i * 32 + w] + __popc(kept[i] & ((1u << lane) - 1u));
-      if (r < rows) pos[r] = keep ? at : kIgnored;
-      if (keep) kept_row[at] = r;
-    }
-    done = total;
-    __syncthreads();
   }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) warp_max[w] = top;
+  if (lane == 0) {
+    s_before[w] = before;
+    s_all[w] = all;
+    s_top[w] = top;
+  }
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, warp_max[i]);
-    int e = 0;
-    if (fp16 && top > 0.0f && top < INFINITY) {
-      (void)frexpf(top, &e);               // top <= 2^e
-      e = 15 - e;
-      e = e < -100 ? -100 : (e > 100 ? 100 : e);
-    }
-    head[0] = __int_as_float(done);
-    head[1] = ldexpf(1.0f, e);
+  before = all = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    before += s_before[i];
+    all += s_all[i];
+    top = fmaxf(top, s_top[i]);
+  }
+  int e = 0;
+  if (fp16 && top > 0.0f && top < INFINITY) {
+    (void)frexpf(top, &e);               // top <= 2^e
+    e = 15 - e;
+    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+  }
+  const float scale = ldexpf(1.0f, e);
+  if (blockIdx.x == 0 && tid == 0) {
+    head[0] = __int_as_float(all);
+    head[1] = scale;
     head[2] = ldexpf(1.0f, -e);
   }
-}
-
-// The kept rows of x next to each other, and their targets, lse and scaled
-// gradients; the rows up to the next multiple of 256 are zero (they are read as
-// parts of tiles).
-__global__ void __launch_bounds__(256)
-k_xent_gather(int rows_pad, int nv, const int* __restrict__ kept_row, const float* __restrict__ head,
-              const uint4* __restrict__ x, const int64_t* __restrict__ target,
-              const float* __restrict__ lse, const float* __restrict__ dnll, uint4* __restrict__ xk,
-              int* __restrict__ tgt_k, float* __restrict__ lse_k, float* __restrict__ g_k) {
-  griddep_trigger();
-  griddep_wait();
-  const int kept = __float_as_int(__ldcg(head));
-  const float scale = __ldcg(head + 1);
-  const int end = (kept + kTileM - 1) / kTileM * kTileM;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < end; i += gridDim.x * 8) {
-    const int lane = threadIdx.x & 31;
-    const int r = i < kept ? __ldcg(kept_row + i) : -1;
+  // a kept row (r >= 0), or zeros, to row `to` of xk; one warp
+  auto copy_row = [&](int r, int to) {
     for (int v0 = lane; v0 < nv; v0 += 32 * 4) {
       uint4 u[4];
 #pragma unroll
@@ -685,14 +659,38 @@ k_xent_gather(int rows_pad, int nv, const int* __restrict__ kept_row, const floa
         u[j] = r >= 0 && v0 + 32 * j < nv ? __ldg(x + int64_t(r) * nv + v0 + 32 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (v0 + 32 * j < nv) xk[int64_t(i) * nv + v0 + 32 * j] = u[j];
+        if (v0 + 32 * j < nv) xk[int64_t(to) * nv + v0 + 32 * j] = u[j];
     }
-    if (lane == 0 && r >= 0) {
-      tgt_k[i] = int(target[r]);
-      lse_k[i] = lse[r];
-      g_k[i] = dnll[r] * scale;
+  };
+  for (int r0 = start; r0 < end; r0 += 256) {
+    const int r = r0 + tid;
+    const int64_t t = r < end ? __ldg(target + r) : -1;
+    const bool keep = t >= 0 && t < vocab;
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    __syncthreads();   // the readers of s_before and s_row are done
+    if (lane == 0) s_before[w] = __popc(kept);
+    __syncthreads();
+    int at = __popc(kept & ((1u << lane) - 1u)), here = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at += i < w ? s_before[i] : 0;
+      here += s_before[i];
     }
+    if (r < end) pos[r] = keep ? before + at : kIgnored;
+    if (keep) {
+      s_row[at] = r;
+      tgt_k[before + at] = int(t);
+      lse_k[before + at] = lse[r];
+      g_k[before + at] = dnll[r] * scale;
+    }
+    __syncthreads();
+    for (int i = w; i < here; i += 8) copy_row(s_row[i], before + i);
+    before += here;
   }
+  // dW reads x in blocks of 64 rows: zeros to the end of the last one (dz is zero
+  // there too, but what the workspace held might not be finite)
+  for (int i = all + blockIdx.x * 8 + w; i < (all + kTileK - 1) / kTileK * kTileK; i += gridDim.x * 8)
+    copy_row(-1, i);
 }
 
 // ---------------------------------------------------------------------------
@@ -854,7 +852,6 @@ BwdPlan xent_plan(int64_t rows, int width, int64_t vocab) {
 struct BwdWs {
   float* head;
   int* pos;
-  int* kept_row;
   int* tgt_k;
   float* lse_k;
   float* g_k;
@@ -869,7 +866,6 @@ BwdWs xent_bwd_ws(void* base, int64_t rows, int width, const BwdPlan& p) {
   BwdWs w;
   w.head = c.take<float>(4);
   w.pos = c.take<int>(rows);
-  w.kept_row = c.take<int>(rows);
   w.tgt_k = c.take<int>(p.rows_pad);
   w.lse_k = c.take<float>(p.rows_pad);
   w.g_k = c.take<float>(p.rows_pad);
@@ -918,14 +914,11 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
                        void* ws, cudaStream_t st) {
   const BwdPlan p = xent_plan(rows, width, vocab);
   const BwdWs b = xent_bwd_ws(ws, rows, width, p);
-  rn_status e = launch_pdl(k_xent_scan, dim3(1), dim3(1024), 0, st, int(rows), int(vocab), int(DT == RN_F16),
-                           target, dnll, b.head, b.pos, b.kept_row);
-  if (e != RN_OK) return e;
-  const int wave = 4 * sm_count();
-  const int64_t groups = ceil_div(p.rows_pad, 8);
-  e = launch_pdl(k_xent_gather, dim3(unsigned(groups < wave ? groups : wave)), dim3(256), 0, st,
-                 int(p.rows_pad), width / 8, b.kept_row, b.head, static_cast<const uint4*>(x), target, lse, dnll,
-                 reinterpret_cast<uint4*>(b.xk), b.tgt_k, b.lse_k, b.g_k);
+  // (eight CTAs at least: they share the zero rows)
+  const int64_t most = 2 * sm_count(), per = up(ceil_div(rows, most), 8);
+  rn_status e = launch_pdl(k_xent_pack, dim3(unsigned(std::max<int64_t>(8, ceil_div(rows, per)))), dim3(256), 0, st, int(rows), int(per),
+                           int(vocab), width / 8, int(DT == RN_F16), static_cast<const uint4*>(x), target, lse, dnll,
+                           b.head, b.pos, reinterpret_cast<uint4*>(b.xk), b.tgt_k, b.lse_k, b.g_k);
   if (e != RN_OK) return e;
   const int64_t ld = int64_t(p.chunk) * p.per_piece;
   XentArgs a = {};

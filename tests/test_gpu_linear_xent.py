@@ -152,6 +152,22 @@ def test_pieces_of_the_vocabulary_and_row_invariance(cuda_lib):
     assert only_w[0] is None and torch.equal(bits(only_w[1]), bits(dw))
 
 
+def test_many_rows_with_a_loss_here_and_there(cuda_lib):
+    # several blocks of rows to a CTA of the packing kernel, kept rows in clumps:
+    # the same as the kept rows alone, bitwise
+    rng = np.random.default_rng(10)
+    rows, width, vocab = 90001, 64, 300
+    x, w, t, g = _case(rng, rows, width, vocab, "bf16", ignored=0.0)
+    keep = np.repeat(rng.random(rows // 50 + 1) < 0.1, 50)[:rows]
+    keep[[0, rows - 1]] = True
+    t = torch.where(torch.from_numpy(keep), t, torch.tensor(-100))
+    x, w, t, g, k = (v.cuda() for v in (x, w, t, g, torch.from_numpy(keep)))
+    _, lse = cuda_lib.linear_xent_fwd(x, w, t)
+    dx, dw = cuda_lib.linear_xent_bwd(x, w, t, lse, g)
+    dx2, dw2 = cuda_lib.linear_xent_bwd(x[k].contiguous(), w, t[k].contiguous(), lse[k].contiguous(), g[k].contiguous())
+    assert torch.equal(bits(dx[k]), bits(dx2)) and not bool(dx[~k].any()) and torch.equal(bits(dw), bits(dw2))
+
+
 def test_no_rows(cuda_lib):
     x = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(300, 64, dtype=torch.bfloat16, device="cuda")

@@ -128,7 +128,7 @@ def test_launch_counts(cuda_lib):
     _, lse = rn.linear_xent_fwd(h0, d["table"], d["target"])
     assert lib.rn_last_launches() == 2                       # tiles, join
     rn.linear_xent_bwd(h0, d["table"], d["target"], lse, torch.ones_like(lse))
-    assert lib.rn_last_launches() == 5                       # scan, gather, dz, gradients, fold
+    assert lib.rn_last_launches() == 4                       # pack, dz, gradients, fold
     rn.layernorm_bwd(h0, d["w1"], h0.clone(), m, r)
     assert lib.rn_last_launches() == 2                       # rows, fold
     rn.embed_bwd(d["ids"], h0, 1000)
