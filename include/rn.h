@@ -423,6 +423,9 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
  * ws: device workspace of ws_bytes >= linear_xent_fwd_workspace_bytes(rows,
  * vocab) (two floats for every 128 logits), 16-byte aligned, contents
  * irrelevant.  rows == 0 enqueues nothing.
+ * The kernel's waits for its own copies and products are bounded: if one ran
+ * out (about four seconds), it would return, and this call and every later one
+ * of this operator on the device would give NaN.
  */
 size_t linear_xent_fwd_workspace_bytes(int64_t rows, int64_t vocab);
 rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype dt, const void* x,

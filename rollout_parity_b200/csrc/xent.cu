@@ -103,13 +103,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// r = 1 / (1 + e^(2u)): tanh(u) = 1 - 2r and 1 - tanh(u)^2 = 4r(1 - r); the
-// absolute error of both is a few 2^-24
-__device__ __forceinline__ float half_tail(float u) {
-  float r;
-  const float d = 1.0f + exp2_approx(u * (2.0f * kLog2e));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return r;
+// r = 1 / (1 + e^(2u)): tanh(u) = 1 - 2r and 1 - tanh(u)^2 = 4r(1 - r), the
+// absolute error of both a few 2^-24.  For |u| < 1/8 tanh from its series (to u^7,
+// the next term is 1.3e-9 of it), so that a cap far above the logits leaves them
+// their digits.  Two arguments at a time.
+__device__ __forceinline__ float2 tanh2(float2 u, float2* r_out) {
+  float2 r;
+  const float2 e = mul2(u, bc2(2.0f * kLog2e));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.0f + exp2_approx(e.x)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.0f + exp2_approx(e.y)));
+  const float2 q = mul2(u, u);
+  const float2 p = fma2(fma2(bc2(-17.0f / 315.0f), q, bc2(2.0f / 15.0f)), q, bc2(-1.0f / 3.0f));
+  const float2 s = fma2(mul2(p, q), u, u), t = fma2(bc2(-2.0f), r, bc2(1.0f));
+  *r_out = r;
+  return make_float2(fabsf(u.x) < 0.125f ? s.x : t.x, fabsf(u.y) < 0.125f ? s.y : t.y);
 }
 
 struct TileAt {
@@ -381,7 +388,12 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (!ok) break;
         if (CAP) {
 #pragma unroll
-          for (int i = 0; i < kStatCols; ++i) z[i] = a.cap * fmaf(-2.0f, half_tail(z[i] * a.inv_cap), 1.0f);
+          for (int i = 0; i < kStatCols; i += 2) {
+            float2 r;
+            const float2 s = mul2(bc2(a.cap), tanh2(mul2(make_float2(z[i], z[i + 1]), bc2(a.inv_cap)), &r));
+            z[i] = s.x;
+            z[i + 1] = s.y;
+          }
         }
         const int cols = a.vocab - col0;   // valid columns when less than 128
         if (cols < kStatCols) {
@@ -442,8 +454,8 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           for (int i = 0; i < 16; ++i) {
             float2 z = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), slope = bc2(gp);
             if (CAP) {
-              const float2 h = make_float2(half_tail(z.x * a.inv_cap), half_tail(z.y * a.inv_cap));
-              z = mul2(bc2(a.cap), fma2(bc2(-2.0f), h, bc2(1.0f)));
+              float2 h;
+              z = mul2(bc2(a.cap), tanh2(mul2(z, bc2(a.inv_cap)), &h));
               const float2 f = mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f)));
               slope = mul2(slope, f);
               r[2 * i] = __float_as_uint(f.x);           // (for the target, below)

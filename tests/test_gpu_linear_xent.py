@@ -152,6 +152,27 @@ def test_pieces_of_the_vocabulary_and_row_invariance(cuda_lib):
     assert only_w[0] is None and torch.equal(bits(only_w[1]), bits(dw))
 
 
+@pytest.mark.parametrize("softcap", [0.75, 1e5])
+def test_caps_far_below_and_above_the_logits(cuda_lib, softcap):
+    # 0.75: most logits saturate; 1e5: tanh(z / cap) of tiny arguments, z again but
+    # for roundings relative to itself
+    rng = np.random.default_rng(11)
+    x, w, t, g = _case(rng, 60, 128, 700, "bf16")
+    if softcap < 1:
+        _check(cuda_lib, x, w, t, g, softcap, "bf16")
+        return
+    d = [v.cuda() for v in (x, w, t)]
+    nll, lse = cuda_lib.linear_xent_fwd(*d, softcap)
+    want, wlse = linear_xent(f64(x), f64(w), t.numpy(), None, softcap)
+    zmax = np.abs(f64(x) @ f64(w).T).max(1)
+    # the logits' own error (acc, as in _check), then the quotient, the series'
+    # four roundings and the product: 8 U32 relative to the logit
+    err = (128 / 16 + 17) * 4 * U32 * (np.abs(f64(x)) @ np.abs(f64(w)).T).max(1) + 8 * U32 * zmax
+    assert_close(lse, wlse, err + 200 * U32 + 2 * U32 * np.abs(wlse), "lse")
+    kept = (t.numpy() >= 0) & (t.numpy() < 700)
+    assert_close(nll, want, np.where(kept, 2 * err + 200 * U32 + 2 * U32 * np.abs(wlse), 0), "nll")
+
+
 def test_many_rows_with_a_loss_here_and_there(cuda_lib):
     # several blocks of rows to a CTA of the packing kernel, kept rows in clumps:
     # the same as the kept rows alone, bitwise
