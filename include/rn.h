@@ -1,6 +1,7 @@
 /*
  * rn.h -- C ABI of librn: batch-invariant zero-centred and gated RMSNorm,
- * forward and backward, for NVIDIA B200 (sm_100a).
+ * forward and backward, for NVIDIA B200 (sm_100a); and layer norm, the embedding
+ * and the linear cross entropy, described at their declarations.
  *
  * The operators
  * -------------
