@@ -45,9 +45,10 @@ constexpr int kIgnored = -1;
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kHalf = 16384;                             // a CTA's half of A or B, a stage
 constexpr int kStages = 6, kStageBytes = 2 * kHalf;      // 192 KB
-constexpr int kThreads = 384;                            // loader, MMA, two idle, eight epilogue warps
+constexpr int kThreads = 384;                            // loader, MMA, two for target logits, eight epilogue warps
 constexpr int kOutBytes = 4096;                          // a warp's part of the result: 32 rows of 128 bytes
-constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
+constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256 + 2 * 128 * 4;
+constexpr int kRestRow = 32;                             // see kDz
 constexpr int kStatCols = 128;                           // columns of one (max, sum) of the forward
 // The forward sums K in segments of 1024: the tensor cores cut each addition to
 // the accumulator off instead of rounding it, an error that grows with the
@@ -74,11 +75,15 @@ struct XentArgs {
   int ld;            // columns of dz: chunk * chunks
   float cap;         // 0: none
   float inv_cap;
+  const void* x;           // kFwd
+  const void* w;           // kFwd
   const int64_t* target;   // kFwd
   const float* head;       // backward: [0] kept rows (int), [1] dz scale, [2] 1 / scale
   const int* tgt_k;        // backward, by kept row: target,
   const float* lse_k;      //   lse
-  const float* g_k;        //   dnll * scale
+  const float* g_k;        //   dnll * scale,
+  const float* zt_k;       //   the target's logit (see target_logit)
+  float* lo_k;             // kDz: what the target's dz was rounded by
   void* dz;                // kDz: [rows_pad][ld]
   float2* part;            // kFwd: [ceil(vocab/128)][rows_pad] (max, sum)
   float* zt;               // kFwd: [rows_pad] the target's s
@@ -196,8 +201,55 @@ __device__ __forceinline__ void st_32(void* p, const uint32_t* r) {   // 32 byte
                : "memory");
 }
 
+// x . w of two rows, fp32, by a warp; every lane gets it
+template <int DT>
+__device__ __forceinline__ float warp_dot(const uint4* __restrict__ x, const uint4* __restrict__ w, int nv) {
+  using F = Fmt<DT>;
+  float2 s = bc2(0.0f);
+  for (int v0 = threadIdx.x & 31; v0 < nv; v0 += 32 * 2) {
+    uint4 a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = v0 + 32 * i < nv;
+      a[i] = in ? __ldg(x + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
+      b[i] = in ? __ldg(w + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 f[4], g[4];
+      F::unpack2(a[i], f);
+      F::unpack2(b[i], g);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s = fma2(f[q], g[q], s);
+    }
+  }
+  float t = s.x + s.y;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+// The target's logit of every lane whose row has its target (column `target`, row
+// `row` of x) among the columns at hand (`here`), one row after the other.  The
+// products' own value is short by what the tensor cores cut off, and that is what
+// a likely target's loss and gradient consist of.  (The backward takes it from
+// k_xent_pack.)
+template <int DT>
+__device__ __forceinline__ float target_logit(const XentArgs& a, bool here, int row, int target) {
+  float z = 0.0f;
+  const int nv = a.H / 8, lane = threadIdx.x & 31;
+  for (unsigned m = __ballot_sync(0xffffffffu, here); m; m &= m - 1) {
+    const int l = __ffs(m) - 1;
+    const int r = __shfl_sync(0xffffffffu, row, l), t = __shfl_sync(0xffffffffu, target, l);
+    const float d = warp_dot<DT>(static_cast<const uint4*>(a.x) + int64_t(r) * nv,
+                                 static_cast<const uint4*>(a.w) + int64_t(t) * nv, nv);
+    if (lane == l) z = d;
+  }
+  return z;
+}
+
 // Warp 0 loads the operands' tiles by TMA into a ring of stages, warp 1 of the
-// even CTA issues the MMAs of the pair, and eight warps read the accumulators
+// even CTA issues the MMAs of the pair, warps 2 and 3 form the rows' target
+// logits (kFwd), and eight warps read the accumulators
 // (two of 256 columns in tensor memory, so that the next products run
 // meanwhile) and finish the tile, four warps the left half of the columns and
 // four the right.
@@ -218,6 +270,9 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
   auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
   const uint32_t tmem_slot = bars + 8 * (2 * kStages + 4);
+  auto zt_full = [&](int b) { return bars + 8 * (2 * kStages + 5 + b); };
+  auto zt_empty = [&](int b) { return bars + 8 * (2 * kStages + 7 + b); };
+  auto zt_at = [&](int b, int row) { return bars + 256 + (b * 128 + row) * 4; };   // kFwd: of this CTA's rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   uint32_t* err = &g_wait_failed;
@@ -236,6 +291,8 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), 16);   // the epilogue warps of both CTAs
+      mbar_init(zt_full(b), 2);      // the warps that fill it
+      mbar_init(zt_empty(b), 8);     // this CTA's epilogue warps
     }
     mbar_init_fence();
   }
@@ -326,6 +383,26 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           if (ok) mma_commit_pair(acc_full(b));
         }
       }
+    } else if (MODE == kFwd && warp >= 2) {
+      // the target logits of the tiles' rows, a tile or two ahead of the epilogue:
+      // warp 2 the first 64 of this CTA's rows, warp 3 the others
+      bool ok = true;
+      for (int j = 0; j < count && ok; ++j) {
+        const TileAt p = walk.at(a, j);
+        const int b = j & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(zt_empty(b), ((j >> 1) & 1) ^ 1, err));
+        if (!ok) break;
+#pragma unroll 1
+        for (int h = 0; h < 64; h += 32) {
+          const int local = (warp - 2) * 64 + h + lane, row = p.m0 + int(rank) * 128 + local;
+          const int64_t tg = row < a.rows ? __ldg(a.target + row) : -1;
+          const bool here = tg >= p.n0 && tg < p.n0 + kTileN && tg < a.vocab;
+          const float z = target_logit<DT>(a, here, row, int(tg));
+          if (here) asm volatile("st.shared.f32 [%0], %1;" ::"r"(zt_at(b, local)), "f"(z) : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(zt_full(b));
+      }
     }
     __syncwarp();
   } else {
@@ -386,6 +463,21 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           free_acc();
         }
         if (!ok) break;
+        const int cols = a.vocab - col0;   // valid columns when less than 128
+        const bool act = row < a.rows;
+        const int64_t tg = act ? __ldg(a.target + row) : -1;
+        const bool here = tg >= col0 && tg < col0 + kStatCols && tg < a.vocab;
+        const int at = here ? int(tg - col0) : -1;
+        ok = __all_sync(0xffffffffu, mbar_wait(zt_full(j & 1), (j >> 1) & 1, err));
+        if (!ok) break;
+        if (here) {
+          float zx;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zx) : "r"(zt_at(j & 1, q * 32 + lane)) : "memory");
+#pragma unroll
+          for (int i = 0; i < kStatCols; ++i) z[i] = at == i ? zx : z[i];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(zt_empty(j & 1));
         if (CAP) {
 #pragma unroll
           for (int i = 0; i < kStatCols; i += 2) {
@@ -395,16 +487,12 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             z[i + 1] = s.y;
           }
         }
-        const int cols = a.vocab - col0;   // valid columns when less than 128
         if (cols < kStatCols) {
 #pragma unroll
           for (int i = 0; i < kStatCols; ++i)
             if (i >= cols) z[i] = -INFINITY;
         }
-        const bool act = row < a.rows;
-        const int64_t tg = act ? __ldg(a.target + row) : -1;
-        if (tg >= col0 && tg < col0 + kStatCols && tg < a.vocab) {
-          const int at = int(tg - col0);
+        if (here) {
           float zt = 0.0f;
 #pragma unroll
           for (int i = 0; i < kStatCols; ++i) zt = at == i ? z[i] : zt;
@@ -434,15 +522,33 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           a.part[int64_t(col0 / kStatCols) * a.rows_pad + row] = make_float2(m, u);
         }
       } else if constexpr (MODE == kDz) {
-        const bool act = row < kept;
-        const int tg = act ? __ldcg(a.tgt_k + row) - a.v0 - col0 : -1;
+        // With at most 32 kept rows, row 32 + k holds what the target's dz of row k
+        // was rounded by (x stands there again): it costs nothing in dW's first 64
+        // rows of K, where few rows would not average the rounding out.
+        const bool act = row < kept, rest = kept <= kRestRow && row >= kRestRow && row < kRestRow + kept;
+        const int k = rest ? row - kRestRow : row;
+        const int target = act || rest ? __ldcg(a.tgt_k + k) : -1, tg = target - a.v0 - col0;
         // exp(z - lse) as 2^(z log2e - lse2), and what lse2 was rounded by in the
         // factor (a likely target's p - 1 would lose digits to it)
-        const float lse = act ? __ldcg(a.lse_k + row) : 0.0f, lse2 = lse * kLog2e;
-        const float g = act ? __ldcg(a.g_k + row) : 0.0f;
+        const float lse = act || rest ? __ldcg(a.lse_k + k) : 0.0f, lse2 = lse * kLog2e;
+        const float g = act || rest ? __ldcg(a.g_k + k) : 0.0f;
         const float gp = g * exp2_approx(-fmaf(lse, kLog2e, -lse2));
         const int cols = a.vocab - a.v0 - col0;
+        const bool here = target >= 0 && unsigned(tg) < 128u;
         uint16_t* dst = static_cast<uint16_t*>(a.dz) + int64_t(row) * a.ld + col0;
+        // the target's dz, from its own logit, and what it is rounded by
+        float dt = 0.0f, lo = 0.0f;
+        if (here) {
+          float2 z = bc2(__ldcg(a.zt_k + k)), f = bc2(1.0f);
+          if (CAP) {
+            float2 h;
+            z = mul2(bc2(a.cap), tanh2(mul2(z, bc2(a.inv_cap)), &h));
+            f = mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f)));
+          }
+          dt = (gp * exp2_approx(fmaf(z.x, kLog2e, -lse2)) - g) * f.x;
+          lo = dt - F::pair(F::pack2(dt, 0.0f)).x;
+          if (act) a.lo_k[row] = lo;
+        }
         if (!wait_acc()) break;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -456,26 +562,24 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (CAP) {
               float2 h;
               z = mul2(bc2(a.cap), tanh2(mul2(z, bc2(a.inv_cap)), &h));
-              const float2 f = mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f)));
-              slope = mul2(slope, f);
-              r[2 * i] = __float_as_uint(f.x);           // (for the target, below)
-              r[2 * i + 1] = __float_as_uint(f.y);
+              slope = mul2(slope, mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f))));
             }
             const float2 e = fma2(z, bc2(kLog2e), bc2(-lse2));
             d[i] = mul2(slope, make_float2(exp2_approx(e.x), exp2_approx(e.y)));
-          }
-          if (unsigned(tg - c) < 32u) {   // the target's 1
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (tg == c + 2 * i) d[i].x -= CAP ? g * __uint_as_float(r[2 * i]) : g;
-              if (tg == c + 2 * i + 1) d[i].y -= CAP ? g * __uint_as_float(r[2 * i + 1]) : g;
-            }
           }
           if (!act || cols < c + 32) {    // no row, or no column: exactly nothing
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if (!act || c + 2 * i >= cols) d[i].x = 0.0f;
               if (!act || c + 2 * i + 1 >= cols) d[i].y = 0.0f;
+            }
+          }
+          if (here && unsigned(tg - c) < 32u) {
+            const float v = act ? dt : lo;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (tg == c + 2 * i) d[i].x = v;
+              if (tg == c + 2 * i + 1) d[i].y = v;
             }
           }
 #pragma unroll
@@ -601,11 +705,12 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restri
 // kept rows come before its own: one launch in place of a scan and a gather, 4 us
 // less for few rows.
 // ---------------------------------------------------------------------------
+template <int DT>
 __global__ void __launch_bounds__(256)
 k_xent_pack(int rows, int rows_per_cta, int vocab, int nv, int fp16, const uint4* __restrict__ x,
             const int64_t* __restrict__ target, const float* __restrict__ lse, const float* __restrict__ dnll,
-            float* __restrict__ head, int* __restrict__ pos, uint4* __restrict__ xk, int* __restrict__ tgt_k,
-            float* __restrict__ lse_k, float* __restrict__ g_k) {
+            const uint4* __restrict__ weight, float* __restrict__ head, int* __restrict__ pos, uint4* __restrict__ xk,
+            int* __restrict__ tgt_k, float* __restrict__ lse_k, float* __restrict__ g_k, float* __restrict__ zt_k) {
   griddep_trigger();
   griddep_wait();
   __shared__ int s_before[8], s_all[8], s_row[256];
@@ -696,13 +801,18 @@ k_xent_pack(int rows, int rows_per_cta, int vocab, int nv, int fp16, const uint4
       g_k[before + at] = dnll[r] * scale;
     }
     __syncthreads();
-    for (int i = w; i < here; i += 8) copy_row(s_row[i], before + i);
+    for (int i = w; i < here; i += 8) {
+      copy_row(s_row[i], before + i);
+      if (all <= kRestRow) copy_row(s_row[i], kRestRow + before + i);   // see kDz
+      const float z = warp_dot<DT>(x + int64_t(s_row[i]) * nv, weight + __ldg(target + s_row[i]) * nv, nv);
+      if (lane == 0) zt_k[before + i] = z;
+    }
     before += here;
   }
   // dW reads x in blocks of 64 rows: zeros to the end of the last one (dz is zero
   // there too, but what the workspace held might not be finite)
   for (int i = all + blockIdx.x * 8 + w; i < (all + kTileK - 1) / kTileK * kTileK; i += gridDim.x * 8)
-    copy_row(-1, i);
+    if (all > kRestRow || i < kRestRow || i >= kRestRow + all) copy_row(-1, i);
 }
 
 // ---------------------------------------------------------------------------
@@ -715,6 +825,7 @@ template <int DT>
 __global__ void __launch_bounds__(256)
 k_xent_fold(int rows, int rows_pad, int H, int chunks, int first, int last, const float* __restrict__ slab,
             float* __restrict__ acc, const float* __restrict__ head, const int* __restrict__ pos,
+            const int* __restrict__ tgt_k, const float* __restrict__ lo_k, const uint4* __restrict__ w,
             uint4* __restrict__ dx) {
   using F = Fmt<DT>;
   griddep_trigger();
@@ -743,6 +854,13 @@ k_xent_fold(int rows, int rows_pad, int H, int chunks, int first, int last, cons
     if (last) {
       float2 f[4] = {make_float2(s[0].x, s[0].y), make_float2(s[0].z, s[0].w), make_float2(s[1].x, s[1].y),
                      make_float2(s[1].z, s[1].w)};
+      if (k >= 0) {   // what the target's dz was rounded by
+        float2 wt[4];
+        F::unpack2(__ldg(w + int64_t(__ldcg(tgt_k + k)) * nv + v), wt);
+        const float lo = __ldcg(lo_k + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = fma2(bc2(lo), wt[e], f[e]);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = failed ? bc2(NAN) : mul2(f[e], bc2(inv));
       dx[i] = F::pack2v(f);
@@ -867,6 +985,8 @@ struct BwdWs {
   int* tgt_k;
   float* lse_k;
   float* g_k;
+  float* zt_k;
+  float* lo_k;
   uint16_t* xk;
   uint16_t* dz;
   float* slab;
@@ -881,6 +1001,8 @@ BwdWs xent_bwd_ws(void* base, int64_t rows, int width, const BwdPlan& p) {
   w.tgt_k = c.take<int>(p.rows_pad);
   w.lse_k = c.take<float>(p.rows_pad);
   w.g_k = c.take<float>(p.rows_pad);
+  w.zt_k = c.take<float>(p.rows_pad);
+  w.lo_k = c.take<float>(p.rows_pad);
   w.xk = c.take<uint16_t>(p.rows_pad * width);
   w.dz = c.take<uint16_t>(p.rows_pad * p.chunk * p.per_piece);
   w.slab = c.take<float>(p.rows_pad * width * p.per_piece);
@@ -906,6 +1028,8 @@ rn_status run_xent_fwd(int64_t rows, int width, int64_t vocab, const void* x, co
   a.vocab = int(vocab);
   a.cap = cap;
   a.inv_cap = cap > 0 ? 1.0f / cap : 0.0f;
+  a.x = x;
+  a.w = w;
   a.target = target;
   a.part = f.part;
   a.zt = f.zt;
@@ -928,15 +1052,16 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
   const BwdWs b = xent_bwd_ws(ws, rows, width, p);
   // (eight CTAs at least: they share the zero rows)
   const int64_t most = 2 * sm_count(), per = up(ceil_div(rows, most), 8);
-  rn_status e = launch_pdl(k_xent_pack, dim3(unsigned(std::max<int64_t>(8, ceil_div(rows, per)))), dim3(256), 0, st, int(rows), int(per),
+  rn_status e = launch_pdl(k_xent_pack<DT>, dim3(unsigned(std::max<int64_t>(8, ceil_div(rows, per)))), dim3(256), 0, st, int(rows), int(per),
                            int(vocab), width / 8, int(DT == RN_F16), static_cast<const uint4*>(x), target, lse, dnll,
-                           b.head, b.pos, reinterpret_cast<uint4*>(b.xk), b.tgt_k, b.lse_k, b.g_k);
+                           static_cast<const uint4*>(w), b.head, b.pos, reinterpret_cast<uint4*>(b.xk), b.tgt_k, b.lse_k,
+                           b.g_k, b.zt_k);
   if (e != RN_OK) return e;
   const int64_t ld = int64_t(p.chunk) * p.per_piece;
   XentArgs a = {};
   a.rows = int(rows);
   a.rows_pad = int(p.rows_pad);
-  a.x_rows = int(rows < 128 ? up(rows, 8) : 128);
+  a.x_rows = int(rows <= 64 ? 64 : rows < 128 ? up(rows, 8) : 128);   // (rows 32 to 63 may hold rests)
   a.x_odd = rows > 128;
   a.H = width;
   a.vocab = int(vocab);
@@ -948,6 +1073,8 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
   a.tgt_k = b.tgt_k;
   a.lse_k = b.lse_k;
   a.g_k = b.g_k;
+  a.zt_k = b.zt_k;
+  a.lo_k = b.lo_k;
   a.dz = b.dz;
   a.slab = dx ? b.slab : nullptr;
   a.dw = dw;
@@ -977,8 +1104,8 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
       const int64_t n = ceil_div(rows * (width / 8), 256);
       const int64_t cap_grid = int64_t(8) * sm_count();
       e = launch_pdl(k_xent_fold<DT>, dim3(unsigned(n < cap_grid ? n : cap_grid)), dim3(256), 0, st, int(rows),
-                     a.rows_pad, width, a.chunks, int(piece == 0), int(last), b.slab, b.acc, b.head, b.pos,
-                     static_cast<uint4*>(dx));
+                     a.rows_pad, width, a.chunks, int(piece == 0), int(last), b.slab, b.acc, b.head, b.pos, b.tgt_k,
+                     b.lo_k, static_cast<const uint4*>(w), static_cast<uint4*>(dx));
     }
     if (e != RN_OK) return e;
   }

@@ -22,7 +22,7 @@ def _case(rng, rows, width, vocab, dtype, ignored=0.2, spread=2.0):
     return x, w, torch.from_numpy(target), dnll
 
 
-def _check(rn, x, w, target, dnll, softcap, dtype):
+def _check(rn, x, w, target, dnll, softcap, dtype, target_exact=False):
     d = [t.cuda() for t in (x, w, target, dnll)]
     nll, lse = rn.linear_xent_fwd(d[0], d[1], d[2], softcap)
     dx, dw = rn.linear_xent_bwd(d[0], d[1], d[2], lse, d[3], softcap)
@@ -48,6 +48,9 @@ def _check(rn, x, w, target, dnll, softcap, dtype):
     prob[np.arange(len(t))[kept], t[kept]] += np.abs(g[kept]) + np.abs(dz[np.arange(len(t))[kept], t[kept]])
     tiny = 2.0 ** -24 * 2.0 ** -15 * np.abs(g).max() if dtype == "f16" else 2.0 ** -134
     dzerr = (perr * prob + U[dtype] * (np.abs(dz) + perr * prob) + tiny * 2) * kept[:, None]
+    if target_exact:   # the target's dz enters the sums with its rounding's rest, rounded itself
+        i, j = np.arange(len(t))[kept], t[kept]
+        dzerr[i, j] = (perr * prob)[i, j] + U[dtype] ** 2 * (np.abs(dz)[i, j] + (perr * prob)[i, j]) + tiny * 2
     assert_close(dx, rdx, dzerr @ np.abs(w64) + (acc(vocab) + 40 * U32) * (np.abs(dz) @ np.abs(w64)), "dx")
     xk = np.where(kept[:, None], np.abs(x64), 0.0)
     assert_close(dw, rdw, dzerr.T @ xk + (acc(len(t)) + 2 * U32) * (np.abs(dz).T @ xk), "dw")
@@ -62,6 +65,36 @@ def _check(rn, x, w, target, dnll, softcap, dtype):
 def test_losses_and_gradients(cuda_lib, rows, width, vocab, softcap, dtype):
     rng = np.random.default_rng(rows + vocab)
     _check(cuda_lib, *_case(rng, rows, width, vocab, dtype), softcap, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,width,vocab,ignored,softcap", [
+    (1, 264, 3000, 0.0, 0.0), (3, 1048, 2500, 0.0, 9.0), (32, 128, 17000, 0.0, 0.0), (300, 72, 500, 0.9, 4.0)])
+def test_few_rows_keep_the_target_s_gradient(cuda_lib, rows, width, vocab, ignored, softcap, dtype):
+    # up to 32 rows with a loss: the rounding of the target's dz, which few rows do
+    # not average out, is made up for in dx and dw
+    rng = np.random.default_rng(rows)
+    case = _case(rng, rows, width, vocab, dtype, ignored=ignored)
+    assert 0 < int(((case[2] >= 0) & (case[2] < vocab)).sum()) <= 32
+    _check(cuda_lib, *case, softcap, dtype, target_exact=True)
+
+
+def test_confident_targets_in_wide_rows(cuda_lib):
+    # a target's logit of 25 from 4096 products: what the tensor cores cut off it
+    # (1e-5) is not in its loss of 1e-7 to 1e-2
+    rng = np.random.default_rng(12)
+    width, vocab = 4096, 400
+    w = draw(rng, (vocab, width), "bf16", 1 / 64)
+    t = rng.integers(0, vocab, 24)
+    wt = f64(w)[t]
+    x = torch.from_numpy((wt / (wt ** 2).sum(1, keepdims=True) * np.linspace(12, 25, 24)[:, None]).astype(np.float32)).bfloat16()
+    nll, _ = cuda_lib.linear_xent_fwd(x.cuda(), w.cuda(), torch.from_numpy(t).cuda())
+    want, _ = linear_xent(f64(x), f64(w), t)
+    # the target's logit: 4096 products of fp32, 64 to a lane's two sums, 6 joins
+    # (38 U32 of the terms); the others' cut-off moves a loss relative to itself
+    zt = 38 * U32 * (np.abs(f64(x)) * np.abs(wt)).sum(1)
+    others = (4096 / 16 + 17) * 4 * U32 * (np.abs(f64(x)) @ np.abs(f64(w)).T).max(1)
+    assert_close(nll, want, zt * np.minimum(1, 2 * want) + (others + 300 * U32) * want * 2 + 50 * U32, "nll")
 
 
 @pytest.mark.parametrize("rows,width,vocab", [(5, 16384, 300), (9, 2056, 20001), (600, 1600, 9000)])
