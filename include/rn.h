@@ -418,8 +418,11 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
  * may serve).  target: [rows] int64, read, 8-byte aligned.  nll, lse: [rows]
  * fp32, written, one of them may be NULL.  dt is RN_BF16 or RN_F16 (the
  * products run on the tensor cores, with fp32 accumulators); RN_F32 is
- * RN_E_DTYPE.  0 <= rows <= 2^22, 1 <= vocab <= 2^24, softcap finite and not
- * negative, else RN_E_ARG.
+ * RN_E_DTYPE.  0 <= rows <= 2^22, 1 <= vocab <= 2^24, softcap 0 or in
+ * [2^-100, 2^100], else RN_E_ARG.
+ * The target's logit is summed in fp32 apart from the others (the tensor cores
+ * cut their sums off instead of rounding them), so a likely target's loss keeps
+ * its digits.
  * A row's nll and lse are bitwise the same alone or inside any batch.
  * ws: device workspace of ws_bytes >= linear_xent_fwd_workspace_bytes(rows,
  * vocab) (two floats for every 128 logits), 16-byte aligned, contents
@@ -443,6 +446,8 @@ rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype d
  * The logits are computed again, a piece of the vocabulary at a time; dz is
  * rounded once to dt (for RN_F16 scaled by a power of two taken from the
  * largest |dnll|, which the products undo) as an operand of the tensor cores.
+ * What the target's dz was rounded by is added back in dx, and in dw when at
+ * most 32 rows are not ignored.
  * Ignored rows take no part, whatever x, lse and dnll hold there; their rows of
  * dx are zero.  A row's dx is bitwise the same alone or inside any batch of the
  * same largest |dnll| (RN_BF16: any batch); dw is bitwise the same across runs.

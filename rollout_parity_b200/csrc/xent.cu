@@ -510,7 +510,9 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           // exp(z - m) as 2^(z log2e - t) with t = m log2e rounded: one multiply-add
           // an element; what t was rounded by, r, is common to all and taken out of
           // the sum (so the largest element counts as exactly 1)
-          const float t = m * kLog2e, r = fmaf(m, kLog2e, -t);
+          // (a maximum of -inf is put to 0: every exponential is of -inf)
+          const float top = m == -INFINITY ? 0.0f : m;
+          const float t = top * kLog2e, r = fmaf(top, kLog2e, -t);
           float2 s2[4] = {bc2(0.0f), bc2(0.0f), bc2(0.0f), bc2(0.0f)};
 #pragma unroll
           for (int i = 0; i < kStatCols; i += 2) {
@@ -1113,7 +1115,8 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
 }
 
 rn_status xent_checks(int64_t rows, int32_t width, int64_t vocab, rn_dtype dt, float cap) {
-  if (!xent_sizes_ok(rows, vocab) || !std::isfinite(cap) || cap < 0.0f) return RN_E_ARG;
+  // (the cap and its reciprocal far from fp32's ends)
+  if (!xent_sizes_ok(rows, vocab) || !(cap == 0.0f || (cap >= 0x1p-100f && cap <= 0x1p100f))) return RN_E_ARG;
   if (dt != RN_BF16 && dt != RN_F16) return RN_E_DTYPE;
   if (!width_ok(width)) return RN_E_WIDTH;
   return RN_OK;

@@ -206,6 +206,37 @@ def test_caps_far_below_and_above_the_logits(cuda_lib, softcap):
     assert_close(nll, want, np.where(kept, 2 * err + 200 * U32 + 2 * U32 * np.abs(wlse), 0), "nll")
 
 
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_logits_of_minus_infinity(cuda_lib, softcap):
+    # words that a row of w makes impossible: a whole block of 128 columns, the
+    # last ones, single ones (with a cap they stand at its lower end)
+    rng = np.random.default_rng(13)
+    vocab, width = 700, 136
+    x, w, t, _ = _case(rng, 40, width, vocab, "bf16")
+    x[:, 0] = 1.0
+    wz = w.clone()
+    gone = np.zeros(vocab, bool)
+    gone[[3, 300]] = gone[128:256] = gone[620:] = True
+    wz[torch.from_numpy(gone), 0] = float("-inf")
+    d = [v.cuda() for v in (x, wz, t)]
+    nll, lse = cuda_lib.linear_xent_fwd(*d, softcap)
+    kept = (t.numpy() >= 0) & (t.numpy() < vocab)
+    hit = kept & gone[np.where(kept, t.numpy(), 0)]
+    z = f64(x) @ f64(w).T
+    s = np.where(gone, -np.inf, z) if not softcap else softcap * np.where(gone, -1.0, np.tanh(z / softcap))
+    wlse = np.log(np.exp(s - s.max(1, keepdims=True)).sum(1)) + s.max(1)
+    want = np.where(kept, wlse - s[np.arange(40), np.where(kept, t.numpy(), 0)], 0.0)
+    # as in _check
+    zerr = (width / 16 + 17) * 4 * U32 * (np.abs(f64(x)) @ np.abs(f64(w)).T).max(1) + 16 * U32 * softcap
+    serr = zerr + (4 + 120 + 64) * U32 + 2 * U32 * np.abs(wlse)
+    assert_close(lse, wlse, serr, "lse")
+    fin = np.isfinite(want)
+    assert hit.any() and (softcap or not fin[hit].any())
+    got = nll.cpu()
+    assert bool(torch.isposinf(got[torch.from_numpy(~fin)]).all())
+    assert_close(got[torch.from_numpy(fin)], want[fin], np.where(kept, serr + zerr + U32 * np.abs(np.where(fin, want, 0)), 0.0)[fin], "nll")
+
+
 def test_many_rows_with_a_loss_here_and_there(cuda_lib):
     # several blocks of rows to a CTA of the packing kernel, kept rows in clumps:
     # the same as the kept rows alone, bitwise

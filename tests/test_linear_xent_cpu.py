@@ -44,6 +44,8 @@ COMMON = [
     ({}, Status.OK), (dict(dt=DType.F16, cap=30.0), Status.OK), (dict(rows=1 << 22, vocab=1000), Status.OK),
     (dict(rows=-1), Status.E_ARG), (dict(rows=(1 << 22) + 1), Status.E_ARG), (dict(vocab=0), Status.E_ARG),
     (dict(vocab=(1 << 24) + 1), Status.E_ARG), (dict(cap=-1.0), Status.E_ARG), (dict(cap=float("nan")), Status.E_ARG),
+    (dict(cap=2.0 ** -100), Status.OK), (dict(cap=2.0 ** 100), Status.OK), (dict(cap=2.0 ** -101), Status.E_ARG),
+    (dict(cap=2.0 ** 101), Status.E_ARG),
     (dict(cap=float("inf")), Status.E_ARG), (dict(dt=DType.F32), Status.E_DTYPE), (dict(dt=9), Status.E_DTYPE),
     (dict(width=100), Status.E_WIDTH), (dict(width=16392), Status.E_WIDTH), (dict(x=0), Status.E_ARG),
     (dict(w=0), Status.E_ARG), (dict(t=0), Status.E_ARG), (dict(x=P(X, 8)), Status.E_ALIGN),
