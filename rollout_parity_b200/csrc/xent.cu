@@ -45,9 +45,9 @@ constexpr int kIgnored = -1;
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kHalf = 16384;                             // a CTA's half of A or B, a stage
 constexpr int kStages = 6, kStageBytes = 2 * kHalf;      // 192 KB
-constexpr int kThreads = 384;                            // loader, MMA, two for target logits, eight epilogue warps
+constexpr int kThreads = 384;                            // loader, MMA, two idle, eight epilogue warps
 constexpr int kOutBytes = 4096;                          // a warp's part of the result: 32 rows of 128 bytes
-constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256 + 2 * 128 * 4;
+constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
 constexpr int kRestRow = 32;                             // see kDz
 constexpr int kStatCols = 128;                           // columns of one (max, sum) of the forward
 // The forward sums K in segments of 1024: the tensor cores cut each addition to
@@ -57,6 +57,13 @@ constexpr int kStatCols = 128;                           // columns of one (max,
 // in two half of it, in four (of 512) 2.5e-7; but every accumulator read costs
 // the products some 600 cycles (4096 rows: 1.90, 2.0 and 2.19 ms).
 constexpr int kSegment = 16;                             // K blocks
+// What is cut off is toward zero and so shortens every logit; over n additions
+// of 16 products it measured 1.2e-8 to 1.4e-8 n (bf16) and 1.6e-8 n (fp16) of the
+// logit for random terms, up to 3.5e-8 n and 9.7e-8 n for terms of one sign.  The
+// forward's segments are therefore lengthened by 2^-26 n, which also holds the
+// sums between the extremes: nll's relative error at H = 2048 falls from 4e-7 to
+// 5e-8.
+constexpr float kCutOff = 0x1p-26f;
 
 // kFwd: logits and their statistics; kDz: logits and dz; kGrad: dx and dW of dz
 enum TileMode { kFwd, kDz, kGrad };
@@ -75,18 +82,16 @@ struct XentArgs {
   int ld;            // columns of dz: chunk * chunks
   float cap;         // 0: none
   float inv_cap;
-  const void* x;           // kFwd
-  const void* w;           // kFwd
   const int64_t* target;   // kFwd
   const float* head;       // backward: [0] kept rows (int), [1] dz scale, [2] 1 / scale
   const int* tgt_k;        // backward, by kept row: target,
   const float* lse_k;      //   lse
   const float* g_k;        //   dnll * scale,
-  const float* zt_k;       //   the target's logit (see target_logit)
+  const float* zt_k;       //   the target's logit, in fp32 (see warp_dot)
   float* lo_k;             // kDz: what the target's dz was rounded by
   void* dz;                // kDz: [rows_pad][ld]
   float2* part;            // kFwd: [ceil(vocab/128)][rows_pad] (max, sum)
-  float* zt;               // kFwd: [rows_pad] the target's s
+  float* zt;               // kFwd: [rows_pad] the target's s, as the products give it
   float* slab;             // kGrad: [chunks][rows_pad][H], NULL: no dx
   void* dw;                // kGrad: [vocab][H], NULL: no dW
   int dw_32;               // the rows of dW start on 32 bytes
@@ -201,7 +206,9 @@ __device__ __forceinline__ void st_32(void* p, const uint32_t* r) {   // 32 byte
                : "memory");
 }
 
-// x . w of two rows, fp32, by a warp; every lane gets it
+// x . w of two rows, fp32, by a warp; every lane gets it.  A target's logit is
+// formed so, apart: the products' own value is short by what the tensor cores cut
+// off, and that is what a likely target's loss and gradient consist of.
 template <int DT>
 __device__ __forceinline__ float warp_dot(const uint4* __restrict__ x, const uint4* __restrict__ w, int nv) {
   using F = Fmt<DT>;
@@ -228,28 +235,8 @@ __device__ __forceinline__ float warp_dot(const uint4* __restrict__ x, const uin
   for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
 }
-// The target's logit of every lane whose row has its target (column `target`, row
-// `row` of x) among the columns at hand (`here`), one row after the other.  The
-// products' own value is short by what the tensor cores cut off, and that is what
-// a likely target's loss and gradient consist of.  (The backward takes it from
-// k_xent_pack.)
-template <int DT>
-__device__ __forceinline__ float target_logit(const XentArgs& a, bool here, int row, int target) {
-  float z = 0.0f;
-  const int nv = a.H / 8, lane = threadIdx.x & 31;
-  for (unsigned m = __ballot_sync(0xffffffffu, here); m; m &= m - 1) {
-    const int l = __ffs(m) - 1;
-    const int r = __shfl_sync(0xffffffffu, row, l), t = __shfl_sync(0xffffffffu, target, l);
-    const float d = warp_dot<DT>(static_cast<const uint4*>(a.x) + int64_t(r) * nv,
-                                 static_cast<const uint4*>(a.w) + int64_t(t) * nv, nv);
-    if (lane == l) z = d;
-  }
-  return z;
-}
-
 // Warp 0 loads the operands' tiles by TMA into a ring of stages, warp 1 of the
-// even CTA issues the MMAs of the pair, warps 2 and 3 form the rows' target
-// logits (kFwd), and eight warps read the accumulators
+// even CTA issues the MMAs of the pair, and eight warps read the accumulators
 // (two of 256 columns in tensor memory, so that the next products run
 // meanwhile) and finish the tile, four warps the left half of the columns and
 // four the right.
@@ -270,9 +257,6 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
   auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
   const uint32_t tmem_slot = bars + 8 * (2 * kStages + 4);
-  auto zt_full = [&](int b) { return bars + 8 * (2 * kStages + 5 + b); };
-  auto zt_empty = [&](int b) { return bars + 8 * (2 * kStages + 7 + b); };
-  auto zt_at = [&](int b, int row) { return bars + 256 + (b * 128 + row) * 4; };   // kFwd: of this CTA's rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   uint32_t* err = &g_wait_failed;
@@ -291,8 +275,6 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), 16);   // the epilogue warps of both CTAs
-      mbar_init(zt_full(b), 2);      // the warps that fill it
-      mbar_init(zt_empty(b), 8);     // this CTA's epilogue warps
     }
     mbar_init_fence();
   }
@@ -383,26 +365,6 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           if (ok) mma_commit_pair(acc_full(b));
         }
       }
-    } else if (MODE == kFwd && warp >= 2) {
-      // the target logits of the tiles' rows, a tile or two ahead of the epilogue:
-      // warp 2 the first 64 of this CTA's rows, warp 3 the others
-      bool ok = true;
-      for (int j = 0; j < count && ok; ++j) {
-        const TileAt p = walk.at(a, j);
-        const int b = j & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(zt_empty(b), ((j >> 1) & 1) ^ 1, err));
-        if (!ok) break;
-#pragma unroll 1
-        for (int h = 0; h < 64; h += 32) {
-          const int local = (warp - 2) * 64 + h + lane, row = p.m0 + int(rank) * 128 + local;
-          const int64_t tg = row < a.rows ? __ldg(a.target + row) : -1;
-          const bool here = tg >= p.n0 && tg < p.n0 + kTileN && tg < a.vocab;
-          const float z = target_logit<DT>(a, here, row, int(tg));
-          if (here) asm volatile("st.shared.f32 [%0], %1;" ::"r"(zt_at(b, local)), "f"(z) : "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(zt_full(b));
-      }
     }
     __syncwarp();
   } else {
@@ -449,40 +411,32 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       };
 
       if constexpr (MODE == kFwd) {
+        // z / k0: the logits as they stand in the accumulators; k0 is the full
+        // segments' factor (of the only one where there is one), `rest` the last's over it
+        const int last_k = a.H - (segs - 1) * kSegment * kTileK;
+        const float k0 = 1.0f + kCutOff * float((segs > 1 ? kSegment * kTileK : a.H) / 16);
+        const float rest = 1.0f - kCutOff * float((a.H - last_k > 0 ? kSegment * kTileK - last_k : 0) / 16);
         float z[kStatCols];
         for (int sg = 0; sg < segs; ++sg) {
           if (!wait_acc()) break;
+          const float f = sg + 1 < segs ? 1.0f : rest;
 #pragma unroll
           for (int c = 0; c < kStatCols; c += 32) {
             uint32_t r[32];
             tmem_ld32(lanes + (n & 1) * kTileN + c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[c + i] = sg == 0 ? __uint_as_float(r[i]) : __fadd_rn(z[c + i], __uint_as_float(r[i]));
+            for (int i = 0; i < 32; ++i) z[c + i] = sg == 0 ? __uint_as_float(r[i]) : fmaf(__uint_as_float(r[i]), f, z[c + i]);
           }
           free_acc();
         }
         if (!ok) break;
         const int cols = a.vocab - col0;   // valid columns when less than 128
-        const bool act = row < a.rows;
-        const int64_t tg = act ? __ldg(a.target + row) : -1;
-        const bool here = tg >= col0 && tg < col0 + kStatCols && tg < a.vocab;
-        const int at = here ? int(tg - col0) : -1;
-        ok = __all_sync(0xffffffffu, mbar_wait(zt_full(j & 1), (j >> 1) & 1, err));
-        if (!ok) break;
-        if (here) {
-          float zx;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zx) : "r"(zt_at(j & 1, q * 32 + lane)) : "memory");
-#pragma unroll
-          for (int i = 0; i < kStatCols; ++i) z[i] = at == i ? zx : z[i];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(zt_empty(j & 1));
         if (CAP) {
 #pragma unroll
           for (int i = 0; i < kStatCols; i += 2) {
             float2 r;
-            const float2 s = mul2(bc2(a.cap), tanh2(mul2(make_float2(z[i], z[i + 1]), bc2(a.inv_cap)), &r));
+            const float2 s = mul2(bc2(a.cap), tanh2(mul2(make_float2(z[i], z[i + 1]), bc2(a.inv_cap * k0)), &r));
             z[i] = s.x;
             z[i + 1] = s.y;
           }
@@ -492,11 +446,14 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           for (int i = 0; i < kStatCols; ++i)
             if (i >= cols) z[i] = -INFINITY;
         }
-        if (here) {
+        const bool act = row < a.rows;
+        const int64_t tg = act ? __ldg(a.target + row) : -1;
+        if (tg >= col0 && tg < col0 + kStatCols && tg < a.vocab) {
+          const int at = int(tg - col0);
           float zt = 0.0f;
 #pragma unroll
           for (int i = 0; i < kStatCols; ++i) zt = at == i ? z[i] : zt;
-          a.zt[row] = zt;
+          a.zt[row] = CAP ? zt : zt * k0;
         }
         if (act && cols > 0) {
           float mc[4] = {z[0], z[1], z[2], z[3]};
@@ -512,16 +469,17 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           // the sum (so the largest element counts as exactly 1)
           // (a maximum of -inf is put to 0: every exponential is of -inf)
           const float top = m == -INFINITY ? 0.0f : m;
-          const float t = top * kLog2e, r = fmaf(top, kLog2e, -t);
+          const float l2 = CAP ? kLog2e : kLog2e * k0;
+          const float t = top * l2, r = fmaf(top, l2, -t);
           float2 s2[4] = {bc2(0.0f), bc2(0.0f), bc2(0.0f), bc2(0.0f)};
 #pragma unroll
           for (int i = 0; i < kStatCols; i += 2) {
-            const float2 e = fma2(make_float2(z[i], z[i + 1]), bc2(kLog2e), bc2(-t));
+            const float2 e = fma2(make_float2(z[i], z[i + 1]), bc2(l2), bc2(-t));
             s2[(i >> 1) & 3] = __fadd2_rn(s2[(i >> 1) & 3], make_float2(exp2_approx(e.x), exp2_approx(e.y)));
           }
           const float2 u2 = __fadd2_rn(__fadd2_rn(s2[0], s2[1]), __fadd2_rn(s2[2], s2[3]));
           const float u = (u2.x + u2.y) * exp2_approx(-r);
-          a.part[int64_t(col0 / kStatCols) * a.rows_pad + row] = make_float2(m, u);
+          a.part[int64_t(col0 / kStatCols) * a.rows_pad + row] = make_float2(CAP ? m : m * k0, u);
         }
       } else if constexpr (MODE == kDz) {
         // With at most 32 kept rows, row 32 + k holds what the target's dz of row k
@@ -650,8 +608,15 @@ __device__ __forceinline__ float2 join_stats(float2 a, float2 b) {   // (max, su
   return make_float2(m, fmaf(a.y, exp2_approx((a.x - m) * kLog2e), b.y * exp2_approx((b.x - m) * kLog2e)));
 }
 
+// The target's logit is put right here: nll and lse as functions of it have the
+// slopes p - 1 and p, and it moves by some 1e-6 of itself (so the second order
+// is far below fp32).  A warp to a row; in the tile kernel, at the columns of the
+// target, a small vocabulary waited for it (3000 x 400 x 5000 27.6 us, here 23.7; 4000 x 400 x
+// 600 30.9 and 18.4).
+template <int DT>
 __global__ void __launch_bounds__(1024)
-k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restrict__ part,
+k_xent_join(int rows, int rows_pad, int tiles, int vocab, int nv, float cap, float inv_cap,
+            const uint4* __restrict__ x, const uint4* __restrict__ w, const float2* __restrict__ part,
             const float* __restrict__ zt, const int64_t* __restrict__ target, float* __restrict__ nll,
             float* __restrict__ lse) {
   griddep_trigger();
@@ -678,6 +643,16 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restri
     }
   }
   sm[j][lane] = s;
+  const int mine = blockIdx.x * 32 + j;
+  const int64_t t = mine < rows ? __ldg(target + mine) : -1;
+  const bool keep = t >= 0 && t < vocab;
+  float move = 0.0f;   // what the target's logit is more than the products gave
+  if (keep) {
+    float2 z = bc2(warp_dot<DT>(x + int64_t(mine) * nv, w + t * nv, nv)), h;
+    if (cap > 0.0f) z = mul2(bc2(cap), tanh2(mul2(z, bc2(inv_cap)), &h));
+    move = z.x - __ldcg(zt + mine);
+    if (!(fabsf(move) < INFINITY)) move = 0.0f;   // infinite either way
+  }
   __syncthreads();
   // warp j joins row j's groups: lane l holds group l
   s = sm[lane][j];
@@ -686,15 +661,19 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, const float2* __restri
     const float2 o = make_float2(__shfl_down_sync(0xffffffffu, s.x, d), __shfl_down_sync(0xffffffffu, s.y, d));
     if ((lane & (2 * d - 1)) == 0) s = join_stats(s, o);
   }
-  const int mine = blockIdx.x * 32 + j;
   if (lane == 0 && mine < rows) {
     const float l = logf(s.y);
-    const int64_t t = target[mine];
     const bool failed = __ldcg(&g_wait_failed) != 0;
     // (max - s[target]) + log(sum): no cancellation where the target is likely
-    const float loss = t >= 0 && t < vocab ? (s.x - zt[mine]) + l : 0.0f;
+    float loss = 0.0f, all = s.x + l;
+    if (keep) {
+      loss = (s.x - __ldcg(zt + mine)) + l;
+      const float other = -expm1f(-loss);   // 1 - p
+      all = fmaf(1.0f - other, move, all);
+      loss = fmaf(-other, move, loss);
+    }
     if (nll) nll[mine] = failed ? NAN : loss;
-    if (lse) lse[mine] = failed ? NAN : s.x + l;
+    if (lse) lse[mine] = failed ? NAN : all;
   }
 }
 
@@ -1030,8 +1009,6 @@ rn_status run_xent_fwd(int64_t rows, int width, int64_t vocab, const void* x, co
   a.vocab = int(vocab);
   a.cap = cap;
   a.inv_cap = cap > 0 ? 1.0f / cap : 0.0f;
-  a.x = x;
-  a.w = w;
   a.target = target;
   a.part = f.part;
   a.zt = f.zt;
@@ -1042,8 +1019,9 @@ rn_status run_xent_fwd(int64_t rows, int width, int64_t vocab, const void* x, co
   const int64_t tiles = ceil_div(rows, kTileM) * ceil_div(vocab, kTileN);
   e = cap > 0 ? launch_tile<DT, kFwd, true>(m, a, tiles, st) : launch_tile<DT, kFwd, false>(m, a, tiles, st);
   if (e != RN_OK) return e;
-  return launch_pdl(k_xent_join, dim3(unsigned(ceil_div(rows, 32))), dim3(1024), 0, st, a.rows, a.rows_pad,
-                    int(ceil_div(vocab, kStatCols)), a.vocab, f.part, f.zt, target, nll, lse);
+  return launch_pdl(k_xent_join<DT>, dim3(unsigned(ceil_div(rows, 32))), dim3(1024), 0, st, a.rows, a.rows_pad,
+                    int(ceil_div(vocab, kStatCols)), a.vocab, width / 8, a.cap, a.inv_cap,
+                    static_cast<const uint4*>(x), static_cast<const uint4*>(w), f.part, f.zt, target, nll, lse);
 }
 
 template <int DT>
