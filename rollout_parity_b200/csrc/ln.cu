@@ -108,7 +108,7 @@ rn_status layernorm_fwd(int64_t rows, int32_t width, float eps, rn_dtype dt, con
   if (e != RN_OK) return e;
   if (validate_only() || rows == 0) return RN_OK;
   const LnFwdArgs a{rows, width, width / vec_elems(dt), eps, 1.0f / float(width),
-                    (width & (width - 1)) == 0 ? 1 : 0, static_cast<const uint4*>(x), w, b,
+                    static_cast<const uint4*>(x), w, b,
                     static_cast<uint4*>(y), mean, rstd};
   const Sched s = row_sched(width, dt);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -157,7 +157,7 @@ rn_status layernorm_bwd(int64_t rows, int32_t width, rn_dtype dt, const void* x,
   float* pw = p.ctas > 1 ? static_cast<float*>(ws) : dw;
   float* pb = !db ? nullptr : p.ctas > 1 ? pw + size_t(p.ctas) * width : db;
   const LnBwdArgs a{rows, p.block_rows, width, width / vec_elems(dt), 1.0f / float(width),
-                    (width & (width - 1)) == 0 ? 1 : 0, static_cast<const uint4*>(x), w,
+                    static_cast<const uint4*>(x), w,
                     static_cast<const uint4*>(dy), mean, rstd, row_mask, static_cast<uint4*>(dx),
                     pw, pb};
   switch (dt) {

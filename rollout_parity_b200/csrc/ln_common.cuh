@@ -10,7 +10,6 @@ struct LnFwdArgs {
   int64_t rows;
   int H, nv;
   float eps, inv_h;
-  int h_pow2;
   const uint4* x;
   const float* w;
   const float* b;   // NULL: no bias
@@ -24,7 +23,6 @@ struct LnBwdArgs {
   int64_t block_rows;    // rows per CTA, a multiple of its teams
   int H, nv;
   float inv_h;
-  int h_pow2;
   const uint4* x;
   const float* w;
   const uint4* dy;

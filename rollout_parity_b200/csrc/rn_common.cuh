@@ -170,10 +170,8 @@ struct KernelPrep {
 // (the default limit is 48 KB) and returns how many of its CTAs fit on one SM
 // there.  The answer is cached per device in `prep`; on a device number beyond
 // the cache the attribute is set again at every call.
-// `most`, where it is given, is the limit that is set: a kernel launched with
-// several sizes (one `prep` each) would otherwise lower it for the larger ones.
 template <typename Kern>
-int prepare_kernel(Kern kernel, int block, size_t smem, KernelPrep& prep, size_t most = 0) {
+int prepare_kernel(Kern kernel, int block, size_t smem, KernelPrep& prep) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -181,9 +179,8 @@ int prepare_kernel(Kern kernel, int block, size_t smem, KernelPrep& prep, size_t
   }
   const bool cached = dev >= 0 && dev < kMaxDevices;
   if (cached && smem < prep.done[dev].load()) return prep.per_sm[dev].load();
-  const size_t limit = smem > most ? smem : most;
-  if (limit > 48 * 1024)
-    (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(limit));
+  if (smem > 48 * 1024)
+    (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   int nb = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kernel, block, smem) != cudaSuccess ||
       nb <= 0) {
