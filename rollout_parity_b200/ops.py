@@ -41,7 +41,7 @@ def act_code(act) -> Act:
 def _mat(name: str, t: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.device != like.device or t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
+    if t.dtype is not like.dtype or t.shape != like.shape or t.device != like.device:
         raise ValueError(f"{name} must be {tuple(like.shape)} {like.dtype} on {like.device}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     if not t.is_contiguous():
@@ -52,7 +52,7 @@ def _mat(name: str, t: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tens
 def _vec(name: str, t: Optional[torch.Tensor], n: int, device) -> torch.Tensor:
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.device != device or t.dtype != torch.float32 or tuple(t.shape) != (n,) \
+    if t.dtype is not torch.float32 or t.shape != (n,) or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 [{n}] tensor on {device}")
     return t
@@ -459,11 +459,11 @@ def layernorm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor] = 
     if mean is not None:
         _vec("mean", mean, rows, x.device)
     elif want_stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        mean = w.new_empty(rows)
     if rstd is not None:
         _vec("rstd", rstd, rows, x.device)
     elif want_stats:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = w.new_empty(rows)
     _launch("layernorm_fwd", x, stream, rows, width, eps, dt, _ptr(x), _ptr(w), _ptr(b), _ptr(y),
             _ptr(mean), _ptr(rstd))
     return y, mean, rstd
@@ -485,12 +485,11 @@ def layernorm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, mean: torc
     _vec("rstd", rstd, rows, x.device)
     row_mask = _row_mask(row_mask, rows, x.device)
     dx = torch.empty_like(x) if dx is None else _mat("dx", dx, x)
-    dw = torch.empty(width, dtype=torch.float32, device=x.device) if dw is None else \
-        _vec("dw", dw, width, x.device)
+    dw = torch.empty_like(w) if dw is None else _vec("dw", dw, width, x.device)
     if db is not None:
         _vec("db", db, width, x.device)
     elif want_db:
-        db = torch.empty(width, dtype=torch.float32, device=x.device)
+        db = torch.empty_like(w)
     lib = load()
     ws, nws = _buffer(ws, int(lib.layernorm_bwd_workspace_bytes(rows, width, dt)), x.device,
                       stream)
