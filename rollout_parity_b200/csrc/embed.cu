@@ -9,8 +9,8 @@
 // start, a leaf is summed in token order, and a run's leaves are joined by the
 // level-by-level pairwise tree.  So a row of dE depends on its own tokens only,
 // bitwise, wherever they stand in the batch and whatever the other tokens are.
-// Three kernels: k_embed_sort, k_embed_reduce, k_embed_join; the first two also
-// clear the rows of dE that no token has.
+// Three kernels: k_embed_sort (few tokens: k_embed_sort_few), k_embed_reduce and
+// k_embed_join; the first two also clear the rows of dE that no token has.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -264,6 +264,102 @@ k_embed_sort(uint32_t tokens, uint32_t vocab, int passes, int bits, const int64_
   }
 
   if (blockIdx.x == 0 && tid == 0) *ws.long_count = 0;
+}
+
+// Up to 4096 tokens: CTA 0 sorts them in its shared memory, every key in a register
+// over a pass.  The rank of a key in its warp's piece is taken once, with the
+// count, and completed by the prefix sums; no cluster barrier, no pass through
+// global memory.  Measured against the cluster, the whole call: 1000 tokens of 4 KB
+// added to 50021 rows (and the old rows' copy) 98 and 105 us, 2000 of 1 KB to 1000
+// rows 27 and 32; 8192 of 2 KB 82 and 79.
+constexpr int kFewTokens = 4096, kFewGroups = kFewTokens / kSortThreads;
+struct FewShared {
+  uint16_t count[kSortWarps][1 << kDigitBits];
+  uint32_t key[kFewTokens];
+  uint16_t tok[kFewTokens];
+  uint32_t warp_sum[kSortWarps];
+};
+__global__ void __launch_bounds__(kSortThreads)
+k_embed_sort_few(uint32_t tokens, uint32_t vocab, int passes, const int64_t* __restrict__ ids, EmbedWs ws,
+                 uint4* __restrict__ clear, int64_t clear_vecs) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  FewShared& sm = *reinterpret_cast<FewShared*>(smem_raw);
+  griddep_trigger();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x > 0) {
+    const int64_t stride = int64_t(gridDim.x - 1) * kSortThreads;
+    for (int64_t i = int64_t(blockIdx.x - 1) * kSortThreads + tid; i < clear_vecs; i += stride) clear[i] = zero;
+    return;
+  }
+  const unsigned below = (1u << lane) - 1u;
+  const int groups = (tokens + kSortThreads - 1) / kSortThreads;   // of 32 tokens, to a warp
+  const uint32_t p0 = uint32_t(w * groups) * 32 + lane;            // this lane's first position
+  uint32_t k[kFewGroups], off[kFewGroups];
+  uint16_t t[kFewGroups];
+#pragma unroll
+  for (int i = 0; i < kFewGroups; ++i) {
+    const uint32_t p = p0 + 32 * i;
+    const int64_t id = i < groups && p < tokens ? __ldg(ids + p) : -1;
+    k[i] = id >= 0 && id < int64_t(vocab) ? uint32_t(id) : vocab;
+    t[i] = uint16_t(p);
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * kDigitBits;
+    uint4* count = reinterpret_cast<uint4*>(sm.count);
+    for (int i = tid; i < int(sizeof(sm.count) / 16); i += kSortThreads) count[i] = zero;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewGroups; ++i) {
+      if (i >= groups) break;   // uniform
+      const bool in = p0 + 32 * i < tokens;
+      const uint32_t d = (k[i] >> shift) & ((1u << kDigitBits) - 1);
+      const unsigned same = same_digit(d, in);
+      const uint32_t c = sm.count[w][d];
+      off[i] = c + __popc(same & below);
+      __syncwarp();
+      if (in && (same & below) == 0) sm.count[w][d] = uint16_t(c + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    // prefix sums in the order (digit, warp): a thread takes 16 warps of a digit
+    const int d = tid >> 1, w0 = (tid & 1) * 16;
+    uint32_t c[16], mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      c[i] = mine;
+      mine += sm.count[w0 + i][d];
+    }
+    const uint32_t start = block_prefix(mine, sm.warp_sum, &all);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sm.count[w0 + i][d] = uint16_t(start + c[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFewGroups; ++i) {
+      if (i < groups && p0 + 32 * i < tokens) {
+        const uint32_t at = sm.count[w][(k[i] >> shift) & ((1u << kDigitBits) - 1)] + off[i];
+        sm.key[at] = k[i];
+        sm.tok[at] = t[i];
+      }
+    }
+    __syncthreads();
+    if (pass + 1 < passes) {
+#pragma unroll
+      for (int i = 0; i < kFewGroups; ++i) {
+        const uint32_t p = p0 + 32 * i;
+        if (i < groups && p < tokens) {
+          k[i] = sm.key[p];
+          t[i] = sm.tok[p];
+        }
+      }
+    }
+  }
+  for (uint32_t p = tid; p < tokens; p += kSortThreads) {
+    ws.key[0][p] = sm.key[p];
+    ws.tok[0][p] = sm.tok[p];
+  }
+  if (tid == 0) *ws.long_count = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -569,6 +665,14 @@ rn_status launch_sort(int64_t tokens, int64_t vocab, const int64_t* ids, const E
   int bits = 1;
   while ((int64_t(1) << bits) <= vocab) ++bits;   // the largest key is vocab
   const int passes = (bits + kDigitBits - 1) / kDigitBits;
+  if (tokens <= kFewTokens) {
+    *last = 0;
+    static KernelPrep few;
+    const int fit = prepare_kernel(k_embed_sort_few, kSortThreads, sizeof(FewShared), few) * sm_count();
+    return launch_pdl(k_embed_sort_few, dim3(clear ? (fit > 1 ? fit : 2) : 1), dim3(kSortThreads), sizeof(FewShared), st,
+                      uint32_t(tokens), uint32_t(vocab), passes, ids, ws, static_cast<uint4*>(clear),
+                      int64_t(clear_bytes / 16));
+  }
   const int digit = (bits + passes - 1) / passes;
   *last = (passes + 1) & 1;
   static KernelPrep prep;

@@ -70,6 +70,23 @@ def test_many_tokens_and_a_long_run(cuda_lib):
     assert_close(d, want, (32 + 24 + 1) * U32 * mag, "dtable")
 
 
+@pytest.mark.parametrize("tokens", [1024, 1025, 4095, 4096, 4097])
+@pytest.mark.parametrize("vocab", [511, 512, 2 ** 18 - 1, 2 ** 18, 300007])
+def test_sorts_of_few_tokens(cuda_lib, tokens, vocab):
+    # one, two and three digits of nine bits; the sort of one CTA and the cluster's
+    rng = np.random.default_rng(tokens + vocab)
+    ids = np.where(rng.random(tokens) < 0.3, rng.integers(0, 20, tokens), rng.integers(-9, vocab, tokens))
+    ids[: tokens // 3 : 2] = vocab - 1
+    dy = draw(rng, (tokens, 8), "f32")
+    got = cuda_lib.embed_bwd(torch.from_numpy(ids).cuda(), dy.cuda(), vocab)
+    # the same tokens among 5000: every row the same bits, whichever kernel sorts
+    more = np.concatenate([ids, np.full(5000 - tokens, -1)])
+    fill = torch.cat([dy, draw(rng, (5000 - tokens, 8), "f32")])
+    other = cuda_lib.embed_bwd(torch.from_numpy(more).cuda(), fill.cuda(), vocab)
+    assert torch.equal(bits(got), bits(other))
+    assert_close(got, embed_bwd(ids, f64(dy), vocab, 1.0), _grad_bound(ids, f64(dy), vocab, 1.0), "dtable")
+
+
 def test_order_is_the_declared_one(cuda_lib):
     # leaves of 32 tokens summed in token order, joined by the pairwise tree, in
     # fp32 on the host: the same bits
