@@ -213,16 +213,16 @@ template <int DT>
 __device__ __forceinline__ float warp_dot(const uint4* __restrict__ x, const uint4* __restrict__ w, int nv) {
   using F = Fmt<DT>;
   float2 s = bc2(0.0f);
-  for (int v0 = threadIdx.x & 31; v0 < nv; v0 += 32 * 2) {
-    uint4 a[2], b[2];
+  for (int v0 = threadIdx.x & 31; v0 < nv; v0 += 32 * 4) {
+    uint4 a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const bool in = v0 + 32 * i < nv;
       a[i] = in ? __ldg(x + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
       b[i] = in ? __ldg(w + v0 + 32 * i) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       float2 f[4], g[4];
       F::unpack2(a[i], f);
       F::unpack2(b[i], g);
@@ -626,7 +626,7 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, int nv, float cap, flo
   const int row = blockIdx.x * 32 + lane;
   float2 s = make_float2(-INFINITY, 0.0f);
   if (row < rows) {
-    constexpr int kAhead = 16;   // loads in flight, to one rescaling
+    constexpr int kAhead = 20;   // loads in flight, to one rescaling
     for (int t0 = j; t0 < tiles; t0 += 32 * kAhead) {
       float2 v[kAhead];
 #pragma unroll
