@@ -99,8 +99,8 @@ def test_confident_targets_in_wide_rows(cuda_lib):
 
 @pytest.mark.parametrize("rows,width,vocab", [(5, 16384, 300), (9, 2056, 20001), (600, 1600, 9000)])
 def test_several_segments_of_the_width(cuda_lib, rows, width, vocab):
-    # K in segments of 512, narrow tiles (few of them) and wide ones, several
-    # tiles to a pair of CTAs
+    # K in segments of 1024, the last one short, few tiles and several
+    # to a pair of CTAs
     rng = np.random.default_rng(0)
     _check(cuda_lib, *_case(rng, rows, width, vocab, "bf16"), 0.0, "bf16")
 
