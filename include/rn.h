@@ -443,7 +443,8 @@ rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype d
  * lse: [rows] fp32 from linear_xent_fwd with the same softcap, read.  dnll:
  * [rows] fp32, read.  dx: [rows, width] dt, written, or NULL.  dw: [vocab,
  * width] dt, written (every row), or NULL; one of them is given.
- * The logits are computed again, a piece of the vocabulary at a time; dz is
+ * The logits are computed again, bitwise as the forward did, a piece of the
+ * vocabulary at a time, so the probabilities add up to 1; dz is
  * rounded once to dt (for RN_F16 scaled by a power of two taken from the
  * largest |dnll|, which the products undo) as an operand of the tensor cores.
  * What the target's dz was rounded by is added back in dx, and in dw when at

@@ -50,7 +50,7 @@ constexpr int kOutBytes = 4096;                          // a warp's part of the
 constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
 constexpr int kRestRow = 32;                             // see kDz
 constexpr int kStatCols = 128;                           // columns of one (max, sum) of the forward
-// The forward sums K in segments of 1024: the tensor cores cut each addition to
+// The logits sum K in segments of 1024: the tensor cores cut each addition to
 // the accumulator off instead of rounding it, an error that grows with the
 // partial sum and the number of steps; the segments' results are added with
 // rounding.  Relative error of nll at H = 2048 in one segment 1.1e-6 to 1.5e-6,
@@ -60,9 +60,12 @@ constexpr int kSegment = 16;                             // K blocks
 // What is cut off is toward zero and so shortens every logit; over n additions
 // of 16 products it measured 1.2e-8 to 1.4e-8 n (bf16) and 1.6e-8 n (fp16) of the
 // logit for random terms, up to 3.5e-8 n and 9.7e-8 n for terms of one sign.  The
-// forward's segments are therefore lengthened by 2^-26 n, which also holds the
+// segments are therefore lengthened by 2^-26 n, which also holds the
 // sums between the extremes: nll's relative error at H = 2048 falls from 4e-7 to
-// 5e-8.
+// 5e-8.  The backward forms its logits with the same segments and factor: they are
+// the bits that lse was made of, so its probabilities add up to 1.  (In one
+// segment without the factor all but the target's were too small by the same
+// share: at H = 16384 and logits of 30 in fp16 3e-3 for terms of one sign.)
 constexpr float kCutOff = 0x1p-26f;
 
 // kFwd: logits and their statistics; kDz: logits and dz; kGrad: dx and dW of dz
@@ -292,14 +295,14 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int kept = MODE == kFwd ? a.rows : __float_as_int(__ldcg(a.head));
   const TileWalk<MODE> walk(a, kept, blockIdx.x >> 1, gridDim.x >> 1);
   const int count = walk.count();
-  // accumulators of one tile: segments of K in the forward, else one
-  auto segments = [](int kblocks) { return MODE == kFwd ? (kblocks + kSegment - 1) / kSegment : 1; };
+  // accumulators of one tile: segments of K for the logits, else one
+  auto segments = [](int kblocks) { return MODE == kGrad ? 1 : (kblocks + kSegment - 1) / kSegment; };
 
-  // The forward's epilogue holds 128 columns of its row: its two warpgroups take
+  // The logits' epilogue holds 128 columns of its row: its two warpgroups take
   // 224 registers a thread from what the block was launched with (384 x 168 =
   // 64512 >= 128 x 40 + 256 x 224 = 62464).
   if (warp < 4) {
-    if constexpr (MODE == kFwd) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (MODE != kGrad) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       const uint32_t bytes = MODE == kGrad ? 2 * kStageBytes
                                            : 2 * kHalf + a.x_rows * 128 * (1 + a.x_odd);   // of both CTAs
@@ -368,7 +371,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     __syncwarp();
   } else {
-    if constexpr (MODE == kFwd) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (MODE != kGrad) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3;                 // the quarter of tensor memory this warp may read
     const int c0 = ((warp - 4) >> 2) * 128;
     const uint32_t lanes = tmem + (uint32_t(q * 32) << 16) + c0;
@@ -410,15 +413,26 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         ++n;
       };
 
-      if constexpr (MODE == kFwd) {
-        // z / k0: the logits as they stand in the accumulators; k0 is the full
-        // segments' factor (of the only one where there is one), `rest` the last's over it
-        const int last_k = a.H - (segs - 1) * kSegment * kTileK;
-        const float k0 = 1.0f + kCutOff * float((segs > 1 ? kSegment * kTileK : a.H) / 16);
-        const float rest = 1.0f - kCutOff * float((a.H - last_k > 0 ? kSegment * kTileK - last_k : 0) / 16);
-        float z[kStatCols];
-        for (int sg = 0; sg < segs; ++sg) {
-          if (!wait_acc()) break;
+      // The logits of this thread's row and 128 columns, over k0: as they stand in the
+      // accumulators; k0 is the full segments' factor (of the only one where there is
+      // one), `rest` the last's over it.
+      const int last_k = a.H - (segs - 1) * kSegment * kTileK;
+      const float k0 = 1.0f + kCutOff * float((segs > 1 ? kSegment * kTileK : a.H) / 16);
+      const float rest = 1.0f - kCutOff * float((a.H - last_k > 0 ? kSegment * kTileK - last_k : 0) / 16);
+      // the sum of the first `count` >= 1 of a tile's accumulators
+      auto read_logits = [&](float (&z)[kStatCols], int count) {
+        if (!wait_acc()) return;
+#pragma unroll
+        for (int c = 0; c < kStatCols; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(lanes + (n & 1) * kTileN + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[c + i] = __uint_as_float(r[i]);
+        }
+        free_acc();
+        for (int sg = 1; sg < count; ++sg) {
+          if (!wait_acc()) return;
           const float f = sg + 1 < segs ? 1.0f : rest;
 #pragma unroll
           for (int c = 0; c < kStatCols; c += 32) {
@@ -426,10 +440,15 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             tmem_ld32(lanes + (n & 1) * kTileN + c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[c + i] = sg == 0 ? __uint_as_float(r[i]) : fmaf(__uint_as_float(r[i]), f, z[c + i]);
+            for (int i = 0; i < 32; ++i) z[c + i] = fmaf(__uint_as_float(r[i]), f, z[c + i]);
           }
           free_acc();
         }
+      };
+
+      if constexpr (MODE == kFwd) {
+        float z[kStatCols];
+        read_logits(z, segs);
         if (!ok) break;
         const int cols = a.vocab - col0;   // valid columns when less than 128
         if (CAP) {
@@ -485,13 +504,13 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         // With at most 32 kept rows, row 32 + k holds what the target's dz of row k
         // was rounded by (x stands there again): it costs nothing in dW's first 64
         // rows of K, where few rows would not average the rounding out.
-        const bool act = row < kept, rest = kept <= kRestRow && row >= kRestRow && row < kRestRow + kept;
-        const int k = rest ? row - kRestRow : row;
-        const int target = act || rest ? __ldcg(a.tgt_k + k) : -1, tg = target - a.v0 - col0;
+        const bool act = row < kept, again = kept <= kRestRow && row >= kRestRow && row < kRestRow + kept;
+        const int k = again ? row - kRestRow : row;
+        const int target = act || again ? __ldcg(a.tgt_k + k) : -1, tg = target - a.v0 - col0;
         // exp(z - lse) as 2^(z log2e - lse2), and what lse2 was rounded by in the
         // factor (a likely target's p - 1 would lose digits to it)
-        const float lse = act || rest ? __ldcg(a.lse_k + k) : 0.0f, lse2 = lse * kLog2e;
-        const float g = act || rest ? __ldcg(a.g_k + k) : 0.0f;
+        const float lse = act || again ? __ldcg(a.lse_k + k) : 0.0f, lse2 = lse * kLog2e;
+        const float g = act || again ? __ldcg(a.g_k + k) : 0.0f;
         const float gp = g * exp2_approx(-fmaf(lse, kLog2e, -lse2));
         const int cols = a.vocab - a.v0 - col0;
         const bool here = target >= 0 && unsigned(tg) < 128u;
@@ -509,22 +528,31 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           lo = dt - F::pair(F::pack2(dt, 0.0f)).x;
           if (act) a.lo_k[row] = lo;
         }
-        if (!wait_acc()) break;
+        float zs[kStatCols];
+        // the last accumulator is read as it is used: read whole, as the others and as in the
+        // forward, 4096 x 1024 x 50000 took 344 us and not 281
+        if (segs > 1) read_logits(zs, segs - 1);
+        if (!ok || !wait_acc()) break;
+        const float l2 = CAP ? kLog2e : kLog2e * k0;
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < kStatCols; c += 32) {
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
           tmem_ld_wait();
+          if (segs > 1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), rest, zs[c + i]));
+          }
           float2 d[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 z = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), slope = bc2(gp);
             if (CAP) {
               float2 h;
-              z = mul2(bc2(a.cap), tanh2(mul2(z, bc2(a.inv_cap)), &h));
+              z = mul2(bc2(a.cap), tanh2(mul2(z, bc2(a.inv_cap * k0)), &h));
               slope = mul2(slope, mul2(mul2(bc2(4.0f), h), fma2(h, bc2(-1.0f), bc2(1.0f))));
             }
-            const float2 e = fma2(z, bc2(kLog2e), bc2(-lse2));
+            const float2 e = fma2(z, bc2(l2), bc2(-lse2));
             d[i] = mul2(slope, make_float2(exp2_approx(e.x), exp2_approx(e.y)));
           }
           if (!act || cols < c + 32) {    // no row, or no column: exactly nothing
