@@ -18,7 +18,7 @@
 // and joined in an order that depends on V only; dx is summed over chunks of
 // the vocabulary whose size depends on V only, in ascending order.  So nll,
 // lse and dx of a row are bitwise the same alone or inside any batch.  dW sums
-// the kept rows in order, in the tensor cores' fp32 accumulator.
+// the kept rows in order, 16384 at a time in the tensor cores' fp32 accumulator.
 #include <cuda.h>
 
 #include <algorithm>
@@ -67,6 +67,10 @@ constexpr int kSegment = 16;                             // K blocks
 // segment without the factor all but the target's were too small by the same
 // share: at H = 16384 and logits of 30 in fp16 3e-3 for terms of one sign.)
 constexpr float kCutOff = 0x1p-26f;
+// dW sums the kept rows in segments of 16384 for the same reason (2^19 rows of one
+// sign in one segment: 3.3e-3 too small in fp16, 4.5e-3 with its rounding in bf16);
+// dx's chunks of the vocabulary are no longer.
+constexpr int kGradSegment = 256;                        // K blocks
 
 // kFwd: logits and their statistics; kDz: logits and dz; kGrad: dx and dW of dz
 enum TileMode { kFwd, kDz, kGrad };
@@ -295,14 +299,15 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int kept = MODE == kFwd ? a.rows : __float_as_int(__ldcg(a.head));
   const TileWalk<MODE> walk(a, kept, blockIdx.x >> 1, gridDim.x >> 1);
   const int count = walk.count();
-  // accumulators of one tile: segments of K for the logits, else one
-  auto segments = [](int kblocks) { return MODE == kGrad ? 1 : (kblocks + kSegment - 1) / kSegment; };
+  // accumulators of one tile: segments of K (one where K is empty)
+  constexpr int kSeg = MODE == kGrad ? kGradSegment : kSegment;
+  auto segments = [](int kblocks) { return max((kblocks + kSeg - 1) / kSeg, 1); };
 
-  // The logits' epilogue holds 128 columns of its row: its two warpgroups take
+  // The epilogue holds the sums of 128 columns of its row: its two warpgroups take
   // 224 registers a thread from what the block was launched with (384 x 168 =
   // 64512 >= 128 x 40 + 256 x 224 = 62464).
   if (warp < 4) {
-    if constexpr (MODE != kGrad) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       const uint32_t bytes = MODE == kGrad ? 2 * kStageBytes
                                            : 2 * kHalf + a.x_rows * 128 * (1 + a.x_odd);   // of both CTAs
@@ -349,7 +354,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const int segs = segments(p.kblocks);
         int kb = 0;
         for (int sg = 0; sg < segs && ok; ++sg, ++n) {
-          const int b = n & 1, end = sg + 1 < segs ? kb + kSegment : p.kblocks;
+          const int b = n & 1, end = sg + 1 < segs ? kb + kSeg : p.kblocks;
           ok = mbar_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, err);
           if (!ok) break;
           tc_fence_after();
@@ -371,7 +376,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     __syncwarp();
   } else {
-    if constexpr (MODE != kGrad) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3;                 // the quarter of tensor memory this warp may read
     const int c0 = ((warp - 4) >> 2) * 128;
     const uint32_t lanes = tmem + (uint32_t(q * 32) << 16) + c0;
@@ -413,14 +418,14 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         ++n;
       };
 
-      // The logits of this thread's row and 128 columns, over k0: as they stand in the
-      // accumulators; k0 is the full segments' factor (of the only one where there is
-      // one), `rest` the last's over it.
+      // The logits stand in the accumulators over k0, the full segments' factor (of the
+      // only one where there is one), the last one's over k0 / rest.
       const int last_k = a.H - (segs - 1) * kSegment * kTileK;
       const float k0 = 1.0f + kCutOff * float((segs > 1 ? kSegment * kTileK : a.H) / 16);
       const float rest = 1.0f - kCutOff * float((a.H - last_k > 0 ? kSegment * kTileK - last_k : 0) / 16);
-      // the sum of the first `count` >= 1 of a tile's accumulators
-      auto read_logits = [&](float (&z)[kStatCols], int count) {
+      // z: the sum of the first `count` >= 1 of the tile's accumulators, this thread's
+      // row and 128 columns
+      auto read_sums = [&](float (&z)[kStatCols], int count) {
         if (!wait_acc()) return;
 #pragma unroll
         for (int c = 0; c < kStatCols; c += 32) {
@@ -433,7 +438,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         free_acc();
         for (int sg = 1; sg < count; ++sg) {
           if (!wait_acc()) return;
-          const float f = sg + 1 < segs ? 1.0f : rest;
+          const float f = MODE == kGrad || sg + 1 < segs ? 1.0f : rest;
 #pragma unroll
           for (int c = 0; c < kStatCols; c += 32) {
             uint32_t r[32];
@@ -448,7 +453,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 
       if constexpr (MODE == kFwd) {
         float z[kStatCols];
-        read_logits(z, segs);
+        read_sums(z, segs);
         if (!ok) break;
         const int cols = a.vocab - col0;   // valid columns when less than 128
         if (CAP) {
@@ -531,7 +536,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         float zs[kStatCols];
         // the last accumulator is read as it is used: read whole, as the others and as in the
         // forward, 4096 x 1024 x 50000 took 344 us and not 281
-        if (segs > 1) read_logits(zs, segs - 1);
+        if (segs > 1) read_sums(zs, segs - 1);
         if (!ok || !wait_acc()) break;
         const float l2 = CAP ? kLog2e : kLog2e * k0;
 #pragma unroll
@@ -595,13 +600,19 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const float inv = __ldcg(a.head + 2);
         const int v_row = a.v0 + p.m0 + int(rank) * 128 + q * 32;   // the warp's first row
         uint16_t* dst = static_cast<uint16_t*>(a.dw) + int64_t(v_row + lane) * a.H + col0;
-        if (!wait_acc()) break;
+        float zs[kStatCols];
+        if (segs > 1) read_sums(zs, segs - 1);
+        if (!ok || !wait_acc()) break;
         uint32_t w[32];            // 64 columns
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
           tmem_ld32(lanes + (n & 1) * kTileN + c, r);
           tmem_ld_wait();
+          if (segs > 1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fadd_rn(__uint_as_float(r[i]), zs[c + i]));
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i)   // no kept row: the accumulator was never written
             w[c % 64 / 2 + i] = p.kblocks == 0 ? 0u : F::pack2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
@@ -970,6 +981,7 @@ FwdWs xent_fwd_ws(void* base, int64_t rows, int64_t vocab) {
 // A piece is as many chunks as keep dz within 512 MB, at least one (4096 x 2048 x
 // 151936 step: 64 MB pieces 7.05 ms, 256 MB 6.50, 512 MB 6.41).
 constexpr int64_t kMostChunk = 16384, kLeastChunk = 8192, kFewTiles = 64;
+static_assert(kMostChunk <= kGradSegment * kTileK, "dx takes a chunk in one accumulator");
 constexpr int64_t kDzBudget = int64_t(512) << 20;
 struct BwdPlan {
   int64_t rows_pad;

@@ -1,5 +1,5 @@
 """Long sums of the linear cross entropy on the GPU: the logits of its backward
-at wide rows."""
+at wide rows, dW over many rows."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +47,21 @@ def test_backward_s_probabilities_are_the_forward_s(cuda_lib, rows, dtype, width
     if softcap:   # the slopes of the target's logit and the others', 2 / cap apart for each 1 between them
         err += 2 / softcap * zr * (_acc(min(width, 1024)) + 64 * 2.0 ** -26) + 16 * U32
     assert_close(dx[:, 0], np.zeros(rows), f64(g) * err, "dx")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_dw_of_many_rows(cuda_lib, dtype):
+    # w = 0: every probability is 1 / 256, dz is exact in either format, and so dw's
+    # error is that of its sum over 2^19 rows (terms of one sign) and its rounding
+    rng = np.random.default_rng(1)
+    rows, width, vocab, g = 1 << 19, 64, 256, 2.0 ** -4
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    x = torch.from_numpy((0.5 + rng.random((rows, width))).astype(np.float32)).to(dt).cuda()
+    w = torch.zeros(vocab, width, dtype=dt, device="cuda")
+    t = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    nll, lse = cuda_lib.linear_xent_fwd(x, w, t)
+    _, dw = cuda_lib.linear_xent_bwd(x, w, t, lse, torch.full_like(nll, g), want_dx=False)
+    want = np.tile(g / 256 * f64(x.double().sum(0)), (vocab, 1))
+    want[0] *= -255.0
+    # segments of 16384 rows, 32 of them added up with rounding
+    assert_close(dw, want, (_acc(16384) + 32 * U32) * np.abs(want), "dw")
