@@ -511,6 +511,14 @@ rn_status rn_test_set_geometry(int32_t max_ctas, int32_t leaves_per_cta,
 void rn_test_set_validate_only(int32_t on);
 
 /*
+ * Test knob: sets (on != 0) or clears on the current device the flag that a wait
+ * of the linear cross entropy leaves behind when it runs out, so that what
+ * follows one can be tested without one.  The caller orders it against work in
+ * flight (cudaDeviceSynchronize before and after).
+ */
+rn_status rn_test_set_wait_failed(int32_t on);
+
+/*
  * Test entry point: out[i] = the reciprocal the sigmoid uses, for inputs
  * d[i] in [1, 2] (n floats, device pointers; steps = 1 or 2 Newton steps;
  * RN_E_ARG otherwise).  Lets a test compare it with IEEE division over every

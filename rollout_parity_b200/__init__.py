@@ -24,6 +24,7 @@ from .ops import (  # noqa: F401
     rn_fold_rows,
     rn_test_set_geometry,
     rn_test_set_validate_only,
+    rn_test_set_wait_failed,
     rmsnorm_add_bwd,
     rmsnorm_add_fwd,
     rmsnorm_bwd,

@@ -839,14 +839,15 @@ k_xent_pack(int rows, int rows_per_cta, int vocab, int nv, int fp16, const uint4
 // backward: dx from the chunks' products, added in ascending order.  Not the
 // last piece: acc = (acc +) slab 0 + slab 1 + ... by kept row.  Last piece: the
 // same sum, unscaled, rounded and put at the rows' own places, zeros for rows
-// without a loss.
+// without a loss.  After a wait that ran out the last piece's launch makes dx NaN, and
+// dW, whose tiles may be anything then.  Either may be NULL: not wanted.
 // ---------------------------------------------------------------------------
 template <int DT>
 __global__ void __launch_bounds__(256)
 k_xent_fold(int rows, int rows_pad, int H, int chunks, int first, int last, const float* __restrict__ slab,
             float* __restrict__ acc, const float* __restrict__ head, const int* __restrict__ pos,
             const int* __restrict__ tgt_k, const float* __restrict__ lo_k, const uint4* __restrict__ w,
-            uint4* __restrict__ dx) {
+            uint4* __restrict__ dx, int64_t dw_vecs, uint4* __restrict__ dw) {
   using F = Fmt<DT>;
   griddep_trigger();
   griddep_wait();
@@ -854,7 +855,12 @@ k_xent_fold(int rows, int rows_pad, int H, int chunks, int first, int last, cons
   const float inv = __ldcg(head + 2);
   const bool failed = __ldcg(&g_wait_failed) != 0;
   const int nv = H / 8;
-  const int64_t n = int64_t(last ? rows : kept) * nv;
+  if (failed && last && dw != nullptr) {
+    const float2 f[4] = {bc2(NAN), bc2(NAN), bc2(NAN), bc2(NAN)};
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < dw_vecs; i += int64_t(gridDim.x) * 256)
+      dw[i] = F::pack2v(f);
+  }
+  const int64_t n = dx == nullptr ? 0 : int64_t(last ? rows : kept) * nv;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
     const int r = int(i / nv), v = int(i % nv);
     const int k = last ? __ldcg(pos + r) : r;
@@ -1119,13 +1125,14 @@ rn_status run_xent_bwd(int64_t rows, int width, int64_t vocab, const void* x, co
                 : launch_tile<DT, kDz, false>(logits, a, mt * vt, st);
     if (e == RN_OK)
       e = launch_tile<DT, kGrad, false>(grad, a, (dx ? mt * ht * a.chunks : 0) + (dw ? vt * ht : 0), st);
-    if (e == RN_OK && dx) {
-      const bool last = piece + 1 == p.pieces;
-      const int64_t n = ceil_div(rows * (width / 8), 256);
+    const bool last = piece + 1 == p.pieces;
+    if (e == RN_OK && (dx || last)) {
+      const int64_t n = dx ? ceil_div(rows * (width / 8), 256) : 1;
       const int64_t cap_grid = int64_t(8) * sm_count();
       e = launch_pdl(k_xent_fold<DT>, dim3(unsigned(n < cap_grid ? n : cap_grid)), dim3(256), 0, st, int(rows),
                      a.rows_pad, width, a.chunks, int(piece == 0), int(last), b.slab, b.acc, b.head, b.pos, b.tgt_k,
-                     b.lo_k, static_cast<const uint4*>(w), static_cast<uint4*>(dx));
+                     b.lo_k, static_cast<const uint4*>(w), static_cast<uint4*>(dx), vocab * (width / 8),
+                     static_cast<uint4*>(dw));
     }
     if (e != RN_OK) return e;
   }
@@ -1201,6 +1208,13 @@ rn_status linear_xent_bwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype d
   }
   return dt == RN_BF16 ? run_xent_bwd<RN_BF16>(rows, width, vocab, x, w, target, lse, dnll, softcap, dx, dw, ws, st)
                        : run_xent_bwd<RN_F16>(rows, width, vocab, x, w, target, lse, dnll, softcap, dx, dw, ws, st);
+}
+
+rn_status rn_test_set_wait_failed(int32_t on) {
+  if (validate_only()) return RN_OK;
+  const uint32_t v = on ? 1u : 0u;
+  const cudaError_t e = cudaMemcpyToSymbol(g_wait_failed, &v, sizeof v);
+  return e == cudaSuccess ? RN_OK : cuda_failed(int(e));
 }
 
 }  // extern "C"

@@ -625,5 +625,9 @@ def rn_test_set_geometry(max_ctas: int = 0, leaves_per_cta: int = 0, fold_rows: 
     check("rn_test_set_geometry", load().rn_test_set_geometry(max_ctas, leaves_per_cta, fold_rows))
 
 
+def rn_test_set_wait_failed(on: bool) -> None:
+    check("rn_test_set_wait_failed", load().rn_test_set_wait_failed(1 if on else 0))
+
+
 def rn_test_set_validate_only(on: bool) -> None:
     load().rn_test_set_validate_only(1 if on else 0)
