@@ -468,8 +468,8 @@ k_ln_bwd_wide(const LnBwdArgs a) {
     }
     cp_async_wait<S - 1>();
     const bool counts = a.mask == nullptr || __ldg(a.mask + row) != 0;   // uniform in the team
-    // with c = x - mean and h = rstd * w * dy (rstd times g):  g * xh = h * c,
-    // dx = h - mean(h) - c * (rstd^2 * mean(h * c))
+    // with c = x - mean:  xh = rstd * c,  dx = rstd * ((g - mean(g)) - c * (rstd * mean(g * xh)))
+    // (no power of rstd stands alone: every value is of the size of dy or of dx)
     const uint4* sp = mine + sl * (2 * K * B);
     const float rs = ssm[(sl * 2 + 1) * B + tid];
     const float2 mu2 = bc2(-ssm[(sl * 2) * B + tid]), rs2 = bc2(rs);
@@ -483,11 +483,11 @@ k_ln_bwd_wide(const LnBwdArgs a) {
       float2 c1 = bc2(-0.0f), c2 = bc2(-0.0f);   // even and odd elements
 #pragma unroll
       for (int q = 0; q < VE / 2; ++q) {
-        const float2 c = addp(xf[q], mu2), dr = mul2(df[q], rs2), h = mul2(g[q], dr);
-        c1 = addp(c1, h);
-        c2 = fma2(h, c, c2);
+        const float2 xh = mul2(addp(xf[q], mu2), rs2), gd = mul2(g[q], df[q]);
+        c1 = addp(c1, gd);
+        c2 = fma2(gd, xh, c2);
         if (counts) {   // dw and db need no row sum: taken before the barrier
-          aw[k][q] = fma2(dr, c, aw[k][q]);
+          aw[k][q] = fma2(df[q], xh, aw[k][q]);
           ab[k][q] = addp(ab[k][q], df[q]);
         }
       }
@@ -498,18 +498,18 @@ k_ln_bwd_wide(const LnBwdArgs a) {
     wide_sum<2, T>(s, red, phase, team);
     __syncwarp();   // (a team of one warp too: the staged row is read again, not kept in registers)
     const float2 m1 = bc2(-__fmul_rn(s[0], a.inv_h));
-    const float2 m2 = bc2(-__fmul_rn(__fmul_rn(rs, rs), __fmul_rn(s[1], a.inv_h)));
+    const float2 m2 = bc2(-__fmul_rn(rs, __fmul_rn(s[1], a.inv_h)));
     uint4* op = a.dx + row * nv + t;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (EXACT || k * T + t < nv) {   // c and h again from the staged row: no registers to keep them
+      if (EXACT || k * T + t < nv) {   // c and g again from the staged row: no registers to keep them
         float2 xf[VE / 2], df[VE / 2], g[VE / 2];
         F::unpack2(sp[k * B], xf);
         F::unpack2(sp[(K + k) * B], df);
         read_param<VE, T>(wp, k, g);
 #pragma unroll
         for (int q = 0; q < VE / 2; ++q)
-          xf[q] = fma2(addp(xf[q], mu2), m2, addp(mul2(g[q], mul2(df[q], rs2)), m1));
+          xf[q] = mul2(rs2, fma2(addp(xf[q], mu2), m2, addp(mul2(g[q], df[q]), m1)));
         st_stream(op + k * T, F::pack2v(xf));
       }
     }
