@@ -82,6 +82,18 @@ __device__ __forceinline__ float thread_sum(const float2 (&a)[K][VE / 2], int nv
   return pairwise_tree<K>(p);
 }
 
+// sum / H, correctly rounded: the product with the rounded reciprocal and one
+// correction by its residual (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990).  The product alone is off in the last
+// place for some widths (776 among them): a constant row was not its bias then, but
+// off by that times 1 / sqrt(eps).  The other means stay products: their last place
+// is the last place of an output.  (__fdiv_rn here: 16384 x 5120 bf16 60.2 to 61.1 us, 8192 x 1544 fp32 17 to 19;
+// in the backward 88.9 to 100.6.)
+__device__ __forceinline__ float row_mean(float sum, float h, float inv_h) {
+  const float q = __fmul_rn(sum, inv_h);
+  return fabsf(q) < INFINITY ? fmaf(fmaf(-q, h, sum), inv_h, q) : q;
+}
+
 template <int DT, int T, int K, bool EXACT>
 __global__ void __launch_bounds__(fwd_block_of(T, K), fwd_min_blocks_of(T, K))
 k_ln_fwd(const LnFwdArgs a) {
@@ -143,7 +155,7 @@ k_ln_fwd(const LnFwdArgs a) {
     for (int k = 0; k < K; ++k) F::unpack2(*slot(sl, k), xf[k]);
     float sum[1] = {thread_sum<VE, T, K, EXACT, false>(xf, nv, t)};
     team_sum<T, 1>(sum, red, phase, team, NT, 0xffffffffu);
-    const float mu = __fmul_rn(sum[0], a.inv_h);
+    const float mu = row_mean(sum[0], float(a.H), a.inv_h);
     const float2 mu2 = bc2(-mu);
 #pragma unroll
     for (int k = 0; k < K; ++k)
