@@ -412,7 +412,7 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
  * log-probability):
  *   z = x w^T;  s = z when softcap == 0, else softcap * tanh(z / softcap)
  *   lse[r] = log(sum_v exp(s[r, v])),  nll[r] = lse[r] - s[r, target[r]]
- * so -nll is the target's log-probability.  A row whose target is outside
+ * so -nll is the target's log-probability, never above 0.  A row whose target is outside
  * [0, vocab) is ignored: its nll is 0 (lse is written) and it has no gradient.
  * x: [rows, width] dt, read.  w: [vocab, width] dt, read (an embedding table
  * may serve).  target: [rows] int64, read, 8-byte aligned.  nll, lse: [rows]

@@ -710,6 +710,8 @@ k_xent_join(int rows, int rows_pad, int tiles, int vocab, int nv, float cap, flo
       const float other = -expm1f(-loss);   // 1 - p
       all = fmaf(1.0f - other, move, all);
       loss = fmaf(-other, move, loss);
+      // a certain target's sum may come out as 1 - 2^-24 (a NaN stays)
+      loss = loss < 0.0f ? 0.0f : loss;
     }
     if (nll) nll[mine] = failed ? NAN : loss;
     if (lse) lse[mine] = failed ? NAN : all;
