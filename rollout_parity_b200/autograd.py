@@ -1,8 +1,11 @@
 """torch.autograd wrappers over the C entry points (the forward saves rstd; the
-backward reuses it, so the statistic the gradient sees is the forward's)."""
+backward reuses it, so the statistic the gradient sees is the forward's).  The
+gradients are computed outside of autograd: the layer norm, the embedding and the
+linear cross entropy refuse to be differentiated twice."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -74,6 +77,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, mean, rstd = ctx.saved_tensors
         dx, dw, db = ops.layernorm_bwd(x, w, dy.contiguous(), mean, rstd, want_db=ctx.biased)
@@ -91,6 +95,7 @@ class Embedding(torch.autograd.Function):
         return ops.embed_fwd(ids, table, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         return None, ops.embed_bwd(ids, dy.contiguous(), ctx.vocab, ctx.scale), None
@@ -109,6 +114,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return nll
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dnll):
         x, w, target, lse = ctx.saved_tensors
         want_dx, want_dw = ctx.needs_input_grad[:2]
