@@ -210,14 +210,12 @@ k_ln_bwd(const LnBwdArgs a) {
   constexpr int B = ln_bwd_block_of(T);
   constexpr int S = ln_bwd_stages_of(T, K, VE);
   constexpr int NT = B / T;
-  constexpr int W = T > 32 ? T / 32 : 1;
   constexpr int GS = gain_src_of(T, K, VE);
-  // dynamic shared memory: reduction scratch [2][NT][2][W] (T > 32) | gain
-  // [K*T*VE] | stages [S][2][K][B] uint4 (afterwards the teams' partials
-  // [NT][2H] floats) | mean and rstd stages [S][2][B]
+  static_assert(T <= 32, "a team within a warp: its sums need no shared memory");
+  // dynamic shared memory: gain [K*T*VE] | stages [S][2][K][B] uint4 (afterwards
+  // the teams' partials [NT][2H] floats) | mean and rstd stages [S][2][B]
   extern __shared__ float dsm[];
-  float* red = dsm;
-  float* gsm = red + (T > 32 ? 2 * NT * 2 * W : 0);
+  float* gsm = dsm;
   uint4* stg = reinterpret_cast<uint4*>(gsm + (GS == kGainSmem ? K * T * VE : 0));
   float* ssm = reinterpret_cast<float*>(stg + S * 2 * K * B);
   const int tid = threadIdx.x, team = tid / T, t = tid % T;
@@ -288,7 +286,7 @@ k_ln_bwd(const LnBwdArgs a) {
       p2[k] = in ? __fadd_rn(c2.x, c2.y) : -0.0f;
     }
     float s[2] = {pairwise_tree<K>(p1), pairwise_tree<K>(p2)};
-    team_sum<T, 2>(s, red, phase, team, NT, 0xffffffffu);
+    team_sum<T, 2>(s, nullptr, phase, team, NT, 0xffffffffu);
     __syncwarp();   // (a team of one warp too: the staged row is read again, not kept in registers)
     const float2 m1 = bc2(-__fmul_rn(s[0], a.inv_h));
     const float2 m2 = bc2(-__fmul_rn(s[1], a.inv_h));
@@ -320,46 +318,32 @@ k_ln_bwd(const LnBwdArgs a) {
   const bool biased = a.pb != nullptr;
   float4* ow = reinterpret_cast<float4*>(a.pw + int64_t(blockIdx.x) * a.H);
   float4* ob = reinterpret_cast<float4*>(a.pb + (biased ? int64_t(blockIdx.x) * a.H : 0));
-  if constexpr (NT == 1) {
+  const int H4 = a.H / 4;
+  float4* lb = reinterpret_cast<float4*>(stg);   // [NT][2 * H4]
+  __syncthreads();   // every team is done with its staged rows
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = k * T + t;
-      if (EXACT || v < nv) {
+  for (int k = 0; k < K; ++k) {
+    const int v = k * T + t;
+    if (EXACT || v < nv) {
 #pragma unroll
-        for (int q = 0; q < VE / 4; ++q) {
-          ow[v * (VE / 4) + q] = make_float4(aw[k][2 * q].x, aw[k][2 * q].y, aw[k][2 * q + 1].x, aw[k][2 * q + 1].y);
-          if (biased)
-            ob[v * (VE / 4) + q] = make_float4(ab[k][2 * q].x, ab[k][2 * q].y, ab[k][2 * q + 1].x, ab[k][2 * q + 1].y);
-        }
+      for (int q = 0; q < VE / 4; ++q) {
+        float4* at = lb + team * 2 * H4 + v * (VE / 4) + q;
+        at[0] = make_float4(aw[k][2 * q].x, aw[k][2 * q].y, aw[k][2 * q + 1].x, aw[k][2 * q + 1].y);
+        at[H4] = make_float4(ab[k][2 * q].x, ab[k][2 * q].y, ab[k][2 * q + 1].x, ab[k][2 * q + 1].y);
       }
     }
-  } else {
-    const int H4 = a.H / 4;
-    float4* lb = reinterpret_cast<float4*>(stg);   // [NT][2 * H4]
-    __syncthreads();   // every team is done with its staged rows
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = k * T + t;
-      if (EXACT || v < nv) {
-#pragma unroll
-        for (int q = 0; q < VE / 4; ++q) {
-          float4* at = lb + team * 2 * H4 + v * (VE / 4) + q;
-          at[0] = make_float4(aw[k][2 * q].x, aw[k][2 * q].y, aw[k][2 * q + 1].x, aw[k][2 * q + 1].y);
-          at[H4] = make_float4(ab[k][2 * q].x, ab[k][2 * q].y, ab[k][2 * q + 1].x, ab[k][2 * q + 1].y);
-        }
-      }
-    }
-    __syncthreads();
-    // a team without rows holds -0.0, the identity, so every team joins
-    for (int c = tid; c < (biased ? 2 : 1) * H4; c += B) {
-      constexpr int LB = NT <= 4 ? 2 : (NT == 8 ? 3 : (NT == 16 ? 4 : (NT == 32 ? 5 : (NT == 64 ? 6 : 7))));
-      TreeCounter<LB, float4> tc;
+  }
+  __syncthreads();
+  // a team without rows holds -0.0, the identity, so every team joins
+  for (int c = tid; c < (biased ? 2 : 1) * H4; c += B) {
+    constexpr int LB = NT == 8 ? 3 : (NT == 16 ? 4 : (NT == 32 ? 5 : (NT == 64 ? 6 : 7)));
+    static_assert(NT == 1 << LB, "8 to 128 teams");
+    TreeCounter<LB, float4> tc;
 #pragma unroll 8
-      for (int j = 0; j < NT; ++j) tc.push(j, lb[j * 2 * H4 + c]);
-      const float4 r = tc.finish(NT);
-      if (c < H4) ow[c] = r;
-      else ob[c - H4] = r;
-    }
+    for (int j = 0; j < NT; ++j) tc.push(j, lb[j * 2 * H4 + c]);
+    const float4 r = tc.finish(NT);
+    if (c < H4) ow[c] = r;
+    else ob[c - H4] = r;
   }
 }
 

@@ -90,7 +90,7 @@ struct XentArgs {
   float cap;         // 0: none
   float inv_cap;
   const int64_t* target;   // kFwd
-  const float* head;       // backward: [0] kept rows (int), [1] dz scale, [2] 1 / scale
+  const float* head;       // backward: [0] kept rows (int), [1] 1 / dz's scale
   const int* tgt_k;        // backward, by kept row: target,
   const float* lse_k;      //   lse
   const float* g_k;        //   dnll * scale,
@@ -597,7 +597,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           }
         }
       } else {                     // dW
-        const float inv = __ldcg(a.head + 2);
+        const float inv = __ldcg(a.head + 1);
         const int v_row = a.v0 + p.m0 + int(rank) * 128 + q * 32;   // the warp's first row
         uint16_t* dst = static_cast<uint16_t*>(a.dw) + int64_t(v_row + lane) * a.H + col0;
         float zs[kStatCols];
@@ -786,8 +786,7 @@ k_xent_pack(int rows, int rows_per_cta, int vocab, int nv, int fp16, const uint4
   const float scale = ldexpf(1.0f, e);
   if (blockIdx.x == 0 && tid == 0) {
     head[0] = __int_as_float(all);
-    head[1] = scale;
-    head[2] = ldexpf(1.0f, -e);
+    head[1] = ldexpf(1.0f, -e);
   }
   // a kept row (r >= 0), or zeros, to row `to` of xk; one warp
   auto copy_row = [&](int r, int to) {
@@ -854,7 +853,7 @@ k_xent_fold(int rows, int rows_pad, int H, int chunks, int first, int last, cons
   griddep_trigger();
   griddep_wait();
   const int kept = __float_as_int(__ldcg(head));
-  const float inv = __ldcg(head + 2);
+  const float inv = __ldcg(head + 1);
   const bool failed = __ldcg(&g_wait_failed) != 0;
   const int nv = H / 8;
   if (failed && last && dw != nullptr) {
@@ -1025,7 +1024,7 @@ struct BwdWs {
 BwdWs xent_bwd_ws(void* base, int64_t rows, int width, const BwdPlan& p) {
   Carve c(base);
   BwdWs w;
-  w.head = c.take<float>(4);
+  w.head = c.take<float>(2);
   w.pos = c.take<int>(rows);
   w.tgt_k = c.take<int>(p.rows_pad);
   w.lse_k = c.take<float>(p.rows_pad);
