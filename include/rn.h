@@ -420,9 +420,12 @@ rn_status embed_bwd(int64_t tokens, int64_t vocab, int32_t width, float scale, r
  * products run on the tensor cores, with fp32 accumulators); RN_F32 is
  * RN_E_DTYPE.  0 <= rows <= 2^22, 1 <= vocab <= 2^24, softcap 0 or in
  * [2^-100, 2^100], else RN_E_ARG.
- * The target's logit is summed in fp32 apart from the others (the tensor cores
- * cut their sums off instead of rounding them), so a likely target's loss keeps
- * its digits.
+ * The tensor cores cut their sums off instead of rounding them; the logits are
+ * lengthened by what that costs on average (2^-26 for every 16 products, 1024 of
+ * them at most).  A logit's error is then up to 9.5e-7 of it where nothing is cut
+ * off (a one-hot x) and up to 1.3e-6 (bf16) or 5.3e-6 (fp16) for products of one
+ * sign.  The target's logit is summed in fp32 apart from the others, so a likely
+ * target's loss keeps its digits.
  * A row's nll and lse are bitwise the same alone or inside any batch.
  * ws: device workspace of ws_bytes >= linear_xent_fwd_workspace_bytes(rows,
  * vocab) (two floats for every 128 logits), 16-byte aligned, contents
@@ -446,9 +449,12 @@ rn_status linear_xent_fwd(int64_t rows, int32_t width, int64_t vocab, rn_dtype d
  * The logits are computed again, bitwise as the forward did, a piece of the
  * vocabulary at a time, so the probabilities add up to 1; dz is
  * rounded once to dt (for RN_F16 scaled by a power of two taken from the
- * largest |dnll|, which the products undo) as an operand of the tensor cores.
+ * largest |dnll|, which the products undo) as an operand of the tensor cores:
+ * dx and dw carry that rounding beside their own.  In RN_F16 what a dz has below
+ * 2^-39 of the largest |dnll| is lost, and below 2^-29 its digits are fewer.
  * What the target's dz was rounded by is added back in dx, and in dw when at
- * most 32 rows are not ignored.
+ * most 32 rows are not ignored.  dw takes its rows 16384 at a time in the tensor
+ * cores' accumulator and adds these sums with rounding.
  * Ignored rows take no part, whatever x, lse and dnll hold there; their rows of
  * dx are zero.  A row's dx is bitwise the same alone or inside any batch of the
  * same largest |dnll| (RN_BF16: any batch); dw is bitwise the same across runs.

@@ -60,9 +60,10 @@ constexpr int kSegment = 16;                             // K blocks
 // What is cut off is toward zero and so shortens every logit; over n additions
 // of 16 products it measured 1.2e-8 to 1.4e-8 n (bf16) and 1.6e-8 n (fp16) of the
 // logit for random terms, up to 3.5e-8 n and 9.7e-8 n for terms of one sign.  The
-// segments are therefore lengthened by 2^-26 n, which also holds the
-// sums between the extremes: nll's relative error at H = 2048 falls from 4e-7 to
-// 5e-8.  The backward forms its logits with the same segments and factor: they are
+// segments are therefore lengthened by 2^-26 n: nll's relative error at H = 2048
+// falls from 4e-7 to 5e-8.  A sum that loses nothing (one-hot rows) is too long by
+// it, 64 x 2^-26 = 9.5e-7 of the logit at H >= 1024; one of terms of one sign stays
+// too short by up to 1.3e-6 (bf16) or 5.3e-6 (fp16).  The backward forms its logits with the same segments and factor: they are
 // the bits that lse was made of, so its probabilities add up to 1.  (In one
 // segment without the factor all but the target's were too small by the same
 // share: at H = 16384 and logits of 30 in fp16 3e-3 for terms of one sign.)

@@ -1,5 +1,5 @@
 """Long sums of the linear cross entropy on the GPU: the logits of its backward
-at wide rows, dW over many rows."""
+at wide rows, dW over many rows, logits without a rounding."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +65,25 @@ def test_dw_of_many_rows(cuda_lib, dtype):
     want[0] *= -255.0
     # segments of 16384 rows, 32 of them added up with rounding
     assert_close(dw, want, (_acc(16384) + 32 * U32) * np.abs(want), "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("width", [1024, 1544, 4096])
+def test_logits_whose_sums_are_exact(cuda_lib, width, dtype):
+    # one element of x: a logit is one product, nothing is cut off, and the factor made
+    # for sums that are (64 additions of 2^-26 at most) is the error, up to 1e-4 here
+    rng = np.random.default_rng(width)
+    rows, vocab = 50, 400
+    w = draw(rng, (vocab, width), dtype)
+    x = torch.zeros(rows, width, dtype=w.dtype)
+    x[torch.arange(rows), torch.from_numpy(rng.integers(0, width, rows))] = torch.linspace(1, 40, rows).to(w.dtype)
+    t = rng.integers(0, vocab, rows)
+    nll, lse = cuda_lib.linear_xent_fwd(x.cuda(), w.cuda(), torch.from_numpy(t).cuda())
+    z = f64(x) @ f64(w).T
+    top = z.max(1, keepdims=True)
+    want = np.log(np.exp(z - top).sum(1)) + top[:, 0]
+    # the factor, and the roundings of the sums (as the tests of the losses have them)
+    err = 64 * 2.0 ** -26 * np.abs(z).max(1) + (4 + 120 + 64) * U32 + 2 * U32 * np.abs(want)
+    assert_close(lse, want, err, "lse")
+    loss = want - z[np.arange(rows), t]
+    assert_close(nll, loss, 2 * err + U32 * loss, "nll")
