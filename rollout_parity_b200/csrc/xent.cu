@@ -46,6 +46,7 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kHalf = 16384;                             // a CTA's half of A or B, a stage
 constexpr int kStages = 6, kStageBytes = 2 * kHalf;      // 192 KB
 constexpr int kThreads = 384;                            // loader, MMA, two idle, eight epilogue warps
+constexpr int kOtherRegs = 40, kEpilogueRegs = 224;      // a thread, of the first four warps and the others
 constexpr int kOutBytes = 4096;                          // a warp's part of the result: 32 rows of 128 bytes
 constexpr int kTileSmem = kStages * kStageBytes + 8 * kOutBytes + 1024 + 256;
 constexpr int kRestRow = 32;                             // see kDz
@@ -305,10 +306,10 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   auto segments = [](int kblocks) { return max((kblocks + kSeg - 1) / kSeg, 1); };
 
   // The epilogue holds the sums of 128 columns of its row: its two warpgroups take
-  // 224 registers a thread from what the block was launched with (384 x 168 =
-  // 64512 >= 128 x 40 + 256 x 224 = 62464).
+  // 224 registers a thread from what the block was launched with (launch_tile checks
+  // that these are enough: with fewer the warpgroups would wait for good).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0 && lane == 0) {
       const uint32_t bytes = MODE == kGrad ? 2 * kStageBytes
                                            : 2 * kHalf + a.x_rows * 128 * (1 + a.x_odd);   // of both CTAs
@@ -377,7 +378,7 @@ k_xent_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
     const int q = warp & 3;                 // the quarter of tensor memory this warp may read
     const int c0 = ((warp - 4) >> 2) * 128;
     const uint32_t lanes = tmem + (uint32_t(q * 32) << 16) + c0;
@@ -943,6 +944,15 @@ template <int DT, int MODE, bool CAP>
 rn_status launch_tile(const TileMaps& m, const XentArgs& a, int64_t most_tiles, cudaStream_t st) {
   static KernelPrep prep;
   (void)prepare_kernel(k_xent_tile<DT, MODE, CAP>, kThreads, kTileSmem, prep);
+  static std::atomic<int> regs{0};   // a thread at launch, of this build
+  if (regs.load() == 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, k_xent_tile<DT, MODE, CAP>);
+    if (e != cudaSuccess) return cuda_failed(int(e));
+    regs.store(fa.numRegs);
+  }
+  if (regs.load() * kThreads < 128 * kOtherRegs + (kThreads - 128) * kEpilogueRegs)
+    return cuda_failed(int(cudaErrorLaunchOutOfResources));
   const int64_t pairs = sm_count() / 2;
   const int64_t want = most_tiles < pairs ? most_tiles : pairs;
   return launch_pdl(k_xent_tile<DT, MODE, CAP>, dim3(unsigned(2 * (want < 1 ? 1 : want))), dim3(kThreads),
