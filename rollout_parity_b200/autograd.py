@@ -1,7 +1,9 @@
 """torch.autograd wrappers over the C entry points (the forward saves rstd; the
 backward reuses it, so the statistic the gradient sees is the forward's).  The
 gradients are computed outside of autograd: the layer norm, the embedding and the
-linear cross entropy refuse to be differentiated twice."""
+linear cross entropy refuse to be differentiated twice.  As with any function of
+torch.autograd, a backward pass is captured into a CUDA graph only while no eager
+graph of the same leaves is alive."""
 from __future__ import annotations
 
 import torch

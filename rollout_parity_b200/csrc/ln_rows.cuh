@@ -46,8 +46,9 @@ struct WideShape {
   int teams, stages;   // teams to a CTA, rows staged to a team
   size_t smem;
 };
-// As many teams as the threads allow with at least two rows of each in shared
-// memory, then as many rows as fit, up to four.
+// As many teams as the threads allow with two rows of each in shared memory, one at
+// least, then as many rows as fit, up to four (fp32 rows from 12288 elements on: one
+// team and one row, so that its load, sums and store take turns).
 __host__ __device__ constexpr WideShape wide_shape(int T, int K, int VE) {
   const size_t params = size_t(K) * VE * T * 4;                 // w
   const size_t row = size_t(2 * K * 16 + 2 * 4) * T;            // x, dy, mean, rstd
@@ -595,7 +596,8 @@ rn_status launch_ln_bwd_wide(const LnBwdArgs& a, int ctas, cudaStream_t st) {
 
 // Rows per backward CTA: about one wave of CTAs on a 148-SM B200 (the number is
 // a constant of the operator, not the device's, so dw does not depend on the
-// device), and at least four steps of the CTA's teams.
+// device), and at least four steps of the CTA's teams: few rows make fewer CTAs than
+// SMs (1000 rows of width 1032 16 of them, of 5120 63).
 inline int64_t ln_rows_of_block(int64_t rows, int teams, int ctas_per_sm) {
   const int64_t wave = int64_t(148) * ctas_per_sm;
   const int64_t per = (rows + wave - 1) / wave;

@@ -6,6 +6,10 @@ allocate outputs the caller did not pass (torch is used for device memory and
 streams only), and call the C ABI on the tensors' device and current stream.
 Every step of the computation runs in librn's kernels; a failed status raises
 RNError.
+
+With ``stream`` the call runs there, but outputs it allocates come from the current
+stream's memory: let ``stream`` wait for the current stream before the call, and
+the current stream for ``stream`` before an output is used or freed.
 """
 from __future__ import annotations
 
