@@ -1,5 +1,5 @@
 """Batch-invariant zero-centred and gated RMSNorm (forward + backward) for B200,
-and under the same contract layer norm, the embedding and the linear cross entropy.
+and layer norm, the embedding and the linear cross entropy.
 
 The computation lives in librn.so (CUDA kernels for sm_100a behind a C ABI,
 declared in include/rn.h).  This package is its thin binding: ``ops`` has one
