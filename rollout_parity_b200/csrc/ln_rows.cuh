@@ -88,8 +88,8 @@ __device__ __forceinline__ float thread_sum(const float2 (&a)[K][VE / 2], int nv
 // the IBM RISC System/6000 processor", 1990).  The product alone is off in the last
 // place for some widths (776 among them): a constant row was not its bias then, but
 // off by that times 1 / sqrt(eps).  The other means stay products: their last place
-// is the last place of an output.  (__fdiv_rn here: 16384 x 5120 bf16 60.2 to 61.1 us, 8192 x 1544 fp32 17 to 19;
-// in the backward 88.9 to 100.6.)
+// is the last place of an output.  (__fdiv_rn here: 16384 x 5120 bf16 60.2 to 61.1
+// us, 8192 x 1544 fp32 17 to 19; in the backward 88.9 to 100.6.)
 __device__ __forceinline__ float row_mean(float sum, float h, float inv_h) {
   const float q = __fmul_rn(sum, inv_h);
   return fabsf(q) < INFINITY ? fmaf(fmaf(-q, h, sum), inv_h, q) : q;

@@ -64,10 +64,11 @@ constexpr int kSegment = 16;                             // K blocks
 // segments are therefore lengthened by 2^-26 n: nll's relative error at H = 2048
 // falls from 4e-7 to 5e-8.  A sum that loses nothing (one-hot rows) is too long by
 // it, 64 x 2^-26 = 9.5e-7 of the logit at H >= 1024; one of terms of one sign stays
-// too short by up to 1.3e-6 (bf16) or 5.3e-6 (fp16).  The backward forms its logits with the same segments and factor: they are
-// the bits that lse was made of, so its probabilities add up to 1.  (In one
-// segment without the factor all but the target's were too small by the same
-// share: at H = 16384 and logits of 30 in fp16 3e-3 for terms of one sign.)
+// too short by up to 1.3e-6 (bf16) or 5.3e-6 (fp16).  The backward forms its logits
+// with the same segments and factor: they are the bits that lse was made of, so its
+// probabilities add up to 1.  (In one segment without the factor all but the
+// target's were too small by the same share: at H = 16384 and logits of 30 in fp16
+// 3e-3 for terms of one sign.)
 constexpr float kCutOff = 0x1p-26f;
 // dW sums the kept rows in segments of 16384 for the same reason (2^19 rows of one
 // sign in one segment: 3.3e-3 too small in fp16, 4.5e-3 with its rounding in bf16);
